@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libgdla.so")
 SOURCES = ["gdla_lib.cu", "gdla_api.cu", "gdla_prefill.cu", "gdla_prefill_bwd.cu", "gdla_prologue.cu", "gdla_decode.cu", "gdla_decode_noalloc.cu",
            "gdla_decode_latent.cu", "gdla_selftest.cu", "gdla_internal.h", "gdla_ptx.cuh", "gdla_prologue.h",
-           "gdla_pair.cuh"]
+           "gdla_pair.cuh", "gdla_paged.cuh", "gdla_cache_append.cu", "gdla_decode_paged.cu"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -118,6 +118,8 @@ namespace {
 
 bool aligned16(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool aligned4(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 struct TileItem {
     int cost;  // key tiles the q-tile visits
     int seq;
@@ -560,6 +562,110 @@ gdla_status_t gdla_attn_decode_latent(const void *q_abs_sig, const void *q_abs_n
     L.out = static_cast<__nv_bfloat16 *>(out);
     L.ws = static_cast<float *>(workspace);
     if (launch_decode_latent(L, plan, static_cast<cudaStream_t>(stream)) != cudaSuccess) return GDLA_ERR_CUDA;
+    return GDLA_OK;
+}
+
+// What both paged-cache calls check of the cache itself.
+static gdla_status_t check_cache(const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale,
+                                 int cache_type, int num_pages, int page_size, const int32_t *block_table,
+                                 int max_pages_per_seq, const int32_t *seqlens_k, int batch, int num_kv_heads) {
+    if (num_kv_heads < 1 || num_kv_heads > GDLA_MAX_KV_HEADS) return GDLA_ERR_UNSUPPORTED;
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return GDLA_ERR_UNSUPPORTED;
+    if (cache_type != GDLA_CACHE_BF16 && cache_type != GDLA_CACHE_E4M3) return GDLA_ERR_INVALID_ARG;
+    if (batch < 1 || num_pages < 1 || max_pages_per_seq < 1) return GDLA_ERR_INVALID_ARG;
+    if (static_cast<long long>(num_pages) * num_kv_heads >= (1ll << 31) ||
+        static_cast<long long>(max_pages_per_seq) * page_size >= (1ll << 31) ||
+        static_cast<long long>(batch) * num_kv_heads >= (1ll << 31))
+        return GDLA_ERR_INVALID_ARG;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(block_table) || !aligned4(seqlens_k))
+        return GDLA_ERR_INVALID_ARG;
+    if (cache_type == GDLA_CACHE_E4M3 && (!aligned4(k_scale) || !aligned4(v_scale))) return GDLA_ERR_INVALID_ARG;
+    return GDLA_OK;
+}
+
+gdla_status_t gdla_cache_append(const void *k_nope, long long k_nope_token_stride, long long k_nope_head_stride,
+                                const void *k_rope, long long k_rope_token_stride, const void *v,
+                                long long v_token_stride, long long v_head_stride, void *k_pages, void *v_pages,
+                                float *k_scale, float *v_scale, int cache_type, int num_pages, int page_size,
+                                const int32_t *block_table, int max_pages_per_seq, const int32_t *cu_seqlens_new,
+                                int num_new_tokens, const int32_t *seqlens_k, int batch, int num_kv_heads, int rotate,
+                                void *stream) {
+    const gdla_status_t st = check_cache(k_pages, v_pages, k_scale, v_scale, cache_type, num_pages, page_size,
+                                         block_table, max_pages_per_seq, seqlens_k, batch, num_kv_heads);
+    if (st != GDLA_OK) return st;
+    const long long strides[] = {k_nope_token_stride, k_nope_head_stride, k_rope_token_stride, v_token_stride,
+                                 v_head_stride};
+    for (long long s : strides)
+        if (s < 0 || (s & 7) != 0) return GDLA_ERR_INVALID_ARG;
+    if (num_new_tokens < 0 || !aligned4(cu_seqlens_new)) return GDLA_ERR_INVALID_ARG;
+    if (num_new_tokens == 0) return GDLA_OK;
+    if (!aligned16(k_nope) || !aligned16(k_rope) || !aligned16(v)) return GDLA_ERR_INVALID_ARG;
+    if (num_new_tokens / page_size + 2ll * batch >= (1ll << 31)) return GDLA_ERR_INVALID_ARG;
+    AppendPlan p{};
+    p.k_nope = static_cast<const __nv_bfloat16 *>(k_nope);
+    p.k_rope = static_cast<const __nv_bfloat16 *>(k_rope);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.nope_token = k_nope_token_stride;
+    p.nope_head = k_nope_head_stride;
+    p.rope_token = k_rope_token_stride;
+    p.v_token = v_token_stride;
+    p.v_head = v_head_stride;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_table = block_table;
+    p.cu_new = cu_seqlens_new;
+    p.seqlens_k = seqlens_k;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_seq;
+    p.num_tokens = num_new_tokens;
+    p.batch = batch;
+    p.hkv = num_kv_heads;
+    p.rotate = rotate != 0;
+    if (launch_cache_append(p, cache_type == GDLA_CACHE_E4M3, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return GDLA_ERR_CUDA;
+    return GDLA_OK;
+}
+
+gdla_status_t gdla_attn_decode_paged(const void *q_sig, const void *q_noise, const void *k_pages, const void *v_pages,
+                                     const float *k_scale, const float *v_scale, int cache_type, int num_pages,
+                                     int page_size, const int32_t *block_table, int max_pages_per_seq,
+                                     const int32_t *seqlens_k, int max_seqlen_k, const float *lambda,
+                                     const void *gate_logits, void *out, int batch, int num_kv_heads, int window,
+                                     int sinks, int rotate, void *stream) {
+    const gdla_status_t st = check_cache(k_pages, v_pages, k_scale, v_scale, cache_type, num_pages, page_size,
+                                         block_table, max_pages_per_seq, seqlens_k, batch, num_kv_heads);
+    if (st != GDLA_OK) return st;
+    if (sinks > GDLA_MAX_SINKS) return GDLA_ERR_UNSUPPORTED;
+    if (sinks < 0 || max_seqlen_k < 1 || max_seqlen_k > static_cast<long long>(max_pages_per_seq) * page_size)
+        return GDLA_ERR_INVALID_ARG;
+    if (!aligned16(q_sig) || !aligned16(q_noise) || !aligned16(lambda) || !aligned16(gate_logits) || !aligned16(out))
+        return GDLA_ERR_INVALID_ARG;
+    PagedDecode p{};
+    p.q_sig = static_cast<const __nv_bfloat16 *>(q_sig);
+    p.q_noise = static_cast<const __nv_bfloat16 *>(q_noise);
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_table = block_table;
+    p.seqlens_k = seqlens_k;
+    p.lambda = lambda;
+    p.gate = static_cast<const __nv_bfloat16 *>(gate_logits);
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_seq;
+    p.max_seqlen_k = max_seqlen_k;
+    p.batch = batch;
+    p.hkv = num_kv_heads;
+    p.window = window;
+    p.sinks = sinks;
+    p.rotate = rotate != 0;
+    if (launch_decode_paged(p, cache_type == GDLA_CACHE_E4M3, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return GDLA_ERR_CUDA;
     return GDLA_OK;
 }
 

@@ -182,6 +182,33 @@ LatentPlan make_latent_plan(int batch, int hkv, int max_seqlen_k, int window, in
 size_t latent_workspace_bytes(const LatentPlan &plan);
 cudaError_t launch_decode_latent(const LatentLaunch &launch, const LatentPlan &plan, cudaStream_t stream);
 
+// Paged KV cache: k_pages [num_pages, H, P, 192] and v_pages [num_pages, H, P, 128] in bf16,
+// or in e4m3 with scales [num_pages, H]; block_table [batch, max_pages] names each
+// sequence's pages in order. All pointers are device memory, strides in elements.
+struct AppendPlan {
+    const __nv_bfloat16 *k_nope, *k_rope, *v;
+    long long nope_token, nope_head, rope_token, v_token, v_head;
+    void *k_pages, *v_pages;
+    float *k_scale, *v_scale;
+    const int32_t *block_table, *cu_new, *seqlens_k;
+    int num_pages, page_size, max_pages, num_tokens, batch, hkv;
+    bool rotate;
+};
+cudaError_t launch_cache_append(const AppendPlan &plan, bool e4m3, cudaStream_t stream);
+
+struct PagedDecode {
+    const __nv_bfloat16 *q_sig, *q_noise;
+    const void *k_pages, *v_pages;
+    const float *k_scale, *v_scale;
+    const int32_t *block_table, *seqlens_k;
+    const float *lambda;
+    const __nv_bfloat16 *gate;
+    __nv_bfloat16 *out;
+    int num_pages, page_size, max_pages, max_seqlen_k, batch, hkv, window, sinks;
+    bool rotate;
+};
+cudaError_t launch_decode_paged(const PagedDecode &plan, bool e4m3, cudaStream_t stream);
+
 // Host-side decode split plan (shared by the workspace query and the launch).
 DecodePlan make_decode_plan(int batch, int hkv, int max_seqlen_k, int window, int num_cache_rows);
 size_t decode_workspace_bytes(const DecodePlan &plan);

@@ -7,4 +7,6 @@
 #include "gdla_decode.cu"
 #include "gdla_decode_noalloc.cu"
 #include "gdla_decode_latent.cu"
+#include "gdla_cache_append.cu"
+#include "gdla_decode_paged.cu"
 #include "gdla_selftest.cu"

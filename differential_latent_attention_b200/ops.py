@@ -22,11 +22,15 @@ STATUS = {0: "GDLA_OK", 1: "GDLA_ERR_INVALID_ARG", 2: "GDLA_ERR_UNSUPPORTED", 3:
           4: "GDLA_ERR_CUDA"}
 EXPORTED = ("gdla_attn_fwd", "gdla_attn_bwd_workspace_bytes", "gdla_attn_bwd", "gdla_prologue_workspace_bytes",
             "gdla_prologue", "gdla_decode_workspace_bytes", "gdla_attn_decode", "gdla_attn_decode_noalloc",
-            "gdla_decode_latent_workspace_bytes", "gdla_attn_decode_latent", "gdla_device_error",
+            "gdla_decode_latent_workspace_bytes", "gdla_attn_decode_latent", "gdla_cache_append",
+            "gdla_attn_decode_paged", "gdla_device_error",
             "gdla_selftest_wait_timeout", "gdla_status_string", "gdla_version")
 DC, DR = 512, 64
 DL = DC + DR
 LATENT_MAX_KV_HEADS = 16
+MAX_SINKS = 128
+PAGE_SIZES = (16, 32, 64, 128)
+CACHE_BF16, CACHE_E4M3 = 0, 1
 SELFTEST_SITE = 0x30001  # GDLA_SELFTEST_SITE
 
 _lib = None
@@ -73,6 +77,12 @@ def library():
             lib.gdla_decode_latent_workspace_bytes.restype = sz
             lib.gdla_attn_decode_latent.argtypes = [p, p, p, p, i, i, p, p, p, p, i, i, i, p, sz, p]
             lib.gdla_attn_decode_latent.restype = i
+            ll = ctypes.c_longlong
+            lib.gdla_cache_append.argtypes = [p, ll, ll, p, ll, p, ll, ll, p, p, p, p, i, i, i, p, i, p, i, p, i, i, i,
+                                              p]
+            lib.gdla_cache_append.restype = i
+            lib.gdla_attn_decode_paged.argtypes = [p, p, p, p, p, p, i, i, i, p, i, p, i, p, p, p, i, i, i, i, i, p]
+            lib.gdla_attn_decode_paged.restype = i
             lib.gdla_device_error.argtypes = [i]
             lib.gdla_device_error.restype = i
             lib.gdla_selftest_wait_timeout.argtypes = [p]
@@ -352,6 +362,113 @@ def attn_decode_latent(q_abs_sig, q_abs_noise, ckv, cu_seqlens_k, max_seqlen_k, 
                                            _stream(stream))
     if st != 0:
         raise GDLAError(st, "gdla_attn_decode_latent")
+    return out
+
+
+def _check_cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k):
+    """The paged cache's own arguments: (cache type, pages, KV heads, page size, batch, table width)."""
+    if not isinstance(k_pages, torch.Tensor) or not isinstance(block_table, torch.Tensor):
+        raise TypeError("k_pages and block_table must be torch.Tensors")
+    if k_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("expected k_pages [pages, H, page_size, 192] and block_table [batch, pages per sequence]")
+    np_, hkv, ps, _ = k_pages.shape
+    b, width = block_table.shape
+    dt = k_pages.dtype
+    if dt is torch.bfloat16:
+        kind = CACHE_BF16
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale belong to an e4m3 cache")
+    elif dt is torch.float8_e4m3fn:
+        kind = CACHE_E4M3
+        _check(k_scale, "k_scale", torch.float32, (np_, hkv))
+        _check(v_scale, "v_scale", torch.float32, (np_, hkv))
+    else:
+        raise TypeError(f"k_pages: expected torch.bfloat16 or torch.float8_e4m3fn, got {dt}")
+    _check(k_pages, "k_pages", dt, (np_, hkv, ps, DQK))
+    _check(v_pages, "v_pages", dt, (np_, hkv, ps, DV))
+    _check(block_table, "block_table", torch.int32, (b, width))
+    _check(seqlens_k, "seqlens_k", torch.int32, (b,))
+    return kind, np_, hkv, ps, b, width
+
+
+def _row_strides(t, name, shape):
+    """Element strides of a bf16 CUDA tensor whose last dimension is dense (others may be views)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name}: its last dimension must be contiguous")
+    st = [0 if size == 1 else x for size, x in zip(shape, st[:-1])]   # one row: its stride says nothing
+    if any(x & 7 for x in st):
+        raise ValueError(f"{name}: strides must be multiples of 8 elements, got {t.stride()}")
+    return st
+
+
+def cache_append(k_nope, k_rope, v, k_pages, v_pages, block_table, cu_seqlens_new, seqlens_k, k_scale=None,
+                 v_scale=None, rotate=True, stream=None):
+    """New keys and values into a paged KV cache (calls ``gdla_cache_append``).
+
+    k_nope [N, H, 128], k_rope [N, 64] (one rotary key for every head) and v [N, H, 128]
+    are bf16, last dimension dense, other strides free (multiples of 8 elements): the
+    prologue's k goes in as ``k[..., :128]`` and ``k[:, 0, 128:]`` with rotate=False.
+    k_pages [P, H, page_size, 192] and v_pages [P, H, page_size, 128] are bf16 or
+    float8_e4m3fn, the latter with k_scale and v_scale fp32 [P, H]. The int32 CUDA
+    tensors block_table [B, W], cu_seqlens_new [B+1] and seqlens_k [B] say where: the
+    rows cu_seqlens_new[b]..cu_seqlens_new[b+1]-1 become the last positions of sequence
+    b, which then holds seqlens_k[b] tokens. ``rotate`` turns k_rope to each token's
+    position on the way. Pages and scales are updated in place.
+    """
+    kind, np_, hkv, ps, b, width = _check_cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k)
+    n = v.shape[0]
+    kn = _row_strides(k_nope, "k_nope", (n, hkv, DQK - DR))
+    kr = _row_strides(k_rope, "k_rope", (n, DR))
+    vs = _row_strides(v, "v", (n, hkv, DV))
+    _check(cu_seqlens_new, "cu_seqlens_new", torch.int32, (b + 1,))
+    _on_one_device(stream, (("k_nope", k_nope), ("k_rope", k_rope), ("v", v), ("k_pages", k_pages),
+                            ("v_pages", v_pages), ("block_table", block_table), ("cu_seqlens_new", cu_seqlens_new),
+                            ("seqlens_k", seqlens_k), ("k_scale", k_scale), ("v_scale", v_scale)))
+    st = library().gdla_cache_append(_ptr(k_nope), kn[0], kn[1], _ptr(k_rope), kr[0], _ptr(v), vs[0], vs[1],
+                                     _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), kind, np_, ps,
+                                     _ptr(block_table), width, _ptr(cu_seqlens_new), n, _ptr(seqlens_k), b, hkv,
+                                     1 if rotate else 0, _stream(stream))
+    if st != 0:
+        raise GDLAError(st, "gdla_cache_append")
+
+
+def attn_decode_paged(q_sig, q_noise, k_pages, v_pages, block_table, seqlens_k, max_seqlen_k, lam, gate, window=0,
+                      sinks=0, k_scale=None, v_scale=None, rotate=False, out=None, stream=None):
+    """GDLA decode over a paged KV cache (calls ``gdla_attn_decode_paged``).
+
+    One query per sequence, at position seqlens_k[b] - 1: q_sig [B, 4H, 192], q_noise
+    [B, H, 192], lam [B, 4H], gate [B, 4H, 128] as for ``attn_decode``; the cache, its
+    scales and block_table as for ``cache_append``. ``window`` > 0 keeps the last window
+    keys and the first ``sinks``; ``rotate`` turns the queries' rotary dims to their
+    position first. Returns out [B, 4H, 128] bf16.
+    """
+    kind, np_, hkv, ps, b, width = _check_cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k)
+    hs = GROUP * hkv
+    _check(q_sig, "q_sig", torch.bfloat16, (b, hs, DQK))
+    _check(q_noise, "q_noise", torch.bfloat16, (b, hkv, DQK))
+    _check(lam, "lam", torch.float32, (b, hs))
+    _check(gate, "gate", torch.bfloat16, (b, hs, DV))
+    if out is None:
+        out = torch.empty((b, hs, DV), dtype=torch.bfloat16, device=q_sig.device)
+    _check(out, "out", torch.bfloat16, (b, hs, DV))
+    _on_one_device(stream, (("q_sig", q_sig), ("q_noise", q_noise), ("k_pages", k_pages), ("v_pages", v_pages),
+                            ("block_table", block_table), ("seqlens_k", seqlens_k), ("lam", lam), ("gate", gate),
+                            ("out", out), ("k_scale", k_scale), ("v_scale", v_scale)))
+    st = library().gdla_attn_decode_paged(_ptr(q_sig), _ptr(q_noise), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+                                          _ptr(v_scale), kind, np_, ps, _ptr(block_table), width, _ptr(seqlens_k),
+                                          int(max_seqlen_k), _ptr(lam), _ptr(gate), _ptr(out), b, hkv, int(window),
+                                          int(sinks), 1 if rotate else 0, _stream(stream))
+    if st != 0:
+        raise GDLAError(st, "gdla_attn_decode_paged")
     return out
 
 

@@ -60,7 +60,12 @@ extern "C" {
 #define GDLA_LATENT_MAX_KV_HEADS 16  /* largest num_kv_heads of the latent-cache decode */
 #define GDLA_DC 512           /* latent (compressed KV) dim */
 #define GDLA_DR 64            /* shared rotary key dim */
+#define GDLA_MAX_SINKS 128    /* most first tokens that stay visible behind a window */
 #define GDLA_VERSION 1
+
+/* Element type of a paged KV cache. */
+#define GDLA_CACHE_BF16 0
+#define GDLA_CACHE_E4M3 1     /* 8-bit codes with one fp32 scale per page and KV head */
 
 typedef enum {
     GDLA_OK = 0,
@@ -280,6 +285,81 @@ GDLA_API gdla_status_t gdla_attn_decode_noalloc(const void *q_sig, const void *q
                                                 int num_cache_rows, int max_seqlen_k, const float *lambda,
                                                 const void *gate_logits, void *out, int batch,
                                                 int num_kv_heads, int window, void *stream);
+
+/*
+ * Paged KV cache: the layout that gdla_cache_append writes and
+ * gdla_attn_decode_paged reads. Pages of page_size (16, 32, 64 or 128) tokens:
+ *   k_pages      [num_pages, num_kv_heads, page_size, 192]   bf16 or e4m3
+ *   v_pages      [num_pages, num_kv_heads, page_size, 128]   the same type
+ *   k_scale, v_scale  fp32 [num_pages, num_kv_heads]: an e4m3 cache's value is
+ *                code * scale of its page and head (NULL for bf16)
+ *   block_table  DEVICE int32 [batch, max_pages_per_seq]: position p of
+ *                sequence b is slot p % page_size of page
+ *                block_table[b][p / page_size]
+ *   seqlens_k    DEVICE int32 [batch], tokens of each sequence in the cache
+ * The lengths and the table are read on the device, so a captured graph can
+ * be replayed while they change.
+ */
+
+/*
+ * Append new keys and values to a paged cache, the rotary key turned to its
+ * position on the way (the pages' rotary key is one 64-wide vector shared by
+ * every KV head; rotate-half form, pairs i, i + 32, base 10000, angles in fp64,
+ * as in gdla_prologue). The new tokens are packed: those of sequence b are rows
+ * cu_seqlens_new[b] .. cu_seqlens_new[b+1]-1 and become its last positions,
+ * seqlens_k[b] counting them already.
+ *   k_nope       bf16, row (t, h) of 128 at k_nope + t * k_nope_token_stride + h * k_nope_head_stride
+ *   k_rope       bf16, row t of 64 at k_rope + t * k_rope_token_stride
+ *   v            bf16, row (t, h) of 128 at v + t * v_token_stride + h * v_head_stride
+ *                (strides in elements, >= 0 and multiples of 8: the prologue's k can
+ *                be given as views of its two parts)
+ *   cu_seqlens_new DEVICE int32 [batch + 1]; num_new_tokens HOST, the rows there are
+ *   rotate       0: k_rope is stored as it is (the prologue's is turned already)
+ * e4m3: scale = 2^e, the smallest (e >= -110) with amax <= 448 * 2^e over the finite
+ * values of the page's tokens. A page that goes on keeps the larger of its own
+ * scale and the new tokens'; if that grows, its older codes are rounded to the new
+ * scale. A page whose slot 0 is written takes the new tokens' scale alone. NaN and
+ * infinities become e4m3's NaN.
+ * Slots that get no token, and pages that no sequence's new tokens fall in, are left
+ * as they were. A sequence whose entries do not fit (a negative count or length, more
+ * positions than its row of the table has, rows outside 0 .. num_new_tokens) and
+ * table entries outside 0 .. num_pages-1 are skipped. A page that this call writes
+ * must belong to one sequence: two that write one page in the same call leave that
+ * page undefined. Inputs and the cache must not overlap.
+ * Errors: GDLA_ERR_INVALID_ARG (null or misaligned pointers, strides, sizes < 1, an
+ * unknown cache_type, num_pages * num_kv_heads or max_pages_per_seq * page_size
+ * >= 2^31), GDLA_ERR_UNSUPPORTED (num_kv_heads or page_size), GDLA_ERR_CUDA.
+ */
+GDLA_API gdla_status_t gdla_cache_append(const void *k_nope, long long k_nope_token_stride,
+                                         long long k_nope_head_stride, const void *k_rope,
+                                         long long k_rope_token_stride, const void *v, long long v_token_stride,
+                                         long long v_head_stride, void *k_pages, void *v_pages, float *k_scale,
+                                         float *v_scale, int cache_type, int num_pages, int page_size,
+                                         const int32_t *block_table, int max_pages_per_seq,
+                                         const int32_t *cu_seqlens_new, int num_new_tokens, const int32_t *seqlens_k,
+                                         int batch, int num_kv_heads, int rotate, void *stream);
+
+/*
+ * Decode over a paged cache: gdla_attn_decode's method, one query per sequence
+ * at position seqlens_k[b] - 1, over the pages of its row of the block table.
+ *   q_sig, q_noise, lambda, gate_logits, out   as for gdla_attn_decode
+ *   max_seqlen_k HOST upper bound on every length, 1 .. max_pages_per_seq * page_size
+ *                (a sequence whose length is not in 1 .. max_seqlen_k gets an all-zero output)
+ *   window       <= 0: every key; > 0: the last `window` keys
+ *   sinks        0 .. GDLA_MAX_SINKS: with a window, the first `sinks` keys stay visible too
+ *   rotate       nonzero: the rotary dims 128..191 of every query are turned to its
+ *                position first (for queries straight from their projection)
+ * Keys whose table entry is outside 0 .. num_pages-1 count as not visible. What a page
+ * holds in slots that are not visible never matters, NaN included.
+ * Errors as for gdla_cache_append, plus GDLA_ERR_UNSUPPORTED for sinks > GDLA_MAX_SINKS.
+ */
+GDLA_API gdla_status_t gdla_attn_decode_paged(const void *q_sig, const void *q_noise, const void *k_pages,
+                                              const void *v_pages, const float *k_scale, const float *v_scale,
+                                              int cache_type, int num_pages, int page_size,
+                                              const int32_t *block_table, int max_pages_per_seq,
+                                              const int32_t *seqlens_k, int max_seqlen_k, const float *lambda,
+                                              const void *gate_logits, void *out, int batch, int num_kv_heads,
+                                              int window, int sinks, int rotate, void *stream);
 
 /*
  * Device-side failure word. Every wait inside the kernels is bounded (about
