@@ -126,11 +126,13 @@ struct TileItem {
     int qt;
 };
 
-// Every (sequence, unit) of `unit_tokens` tokens with its cost (cost(L, unit)),
-// heaviest first, in plans of at most kPlanMaxItems units and kPlanMaxSeqs
-// sequences; launch(plan) for each. Returns false on the first failed launch.
-template <class Cost, class Launch>
-bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int unit_tokens, Cost cost, Launch launch) {
+// Every (sequence, unit) with its cost, heaviest first, in plans of at most
+// kPlanMaxItems units and kPlanMaxSeqs sequences; launch(plan) for each. A sequence of
+// length L has units(L) of them, unit u costs cost(L, u) and is item index(L, u); part[b]
+// (empty: -1) goes with the sequence. Returns false on the first failed launch.
+template <class Units, class Cost, class Index, class Launch>
+bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int sinks, const std::vector<int> &part,
+               Units units, Cost cost, Index index, Launch launch) {
     std::vector<TileItem> items;
     std::vector<int> seq_start(batch);
     long long s0 = 0;
@@ -138,7 +140,7 @@ bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int unit_
         seq_start[b] = static_cast<int>(s0);
         const int L = seqlens[b];
         s0 += L;
-        const int nu = (L + unit_tokens - 1) / unit_tokens;
+        const int nu = units(L);
         for (int u = 0; u < nu; ++u) items.push_back({cost(L, u), b, u});
     }
     std::stable_sort(items.begin(), items.end(), [](const TileItem &a, const TileItem &b) {
@@ -154,6 +156,7 @@ bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int unit_
         P.n_items = 0;
         P.hkv = hkv;
         P.window = window;
+        P.sinks = sinks;
         int n_seq = 0;
         std::vector<int> used;
         while (pos < items.size() && P.n_items < kPlanMaxItems) {
@@ -163,11 +166,12 @@ bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int unit_
                 local[it.seq] = n_seq;
                 P.seq_start[n_seq] = seq_start[it.seq];
                 P.seq_len[n_seq] = seqlens[it.seq];
+                P.part[n_seq] = part.empty() ? -1 : part[it.seq];
                 used.push_back(it.seq);
                 ++n_seq;
             }
             P.items[P.n_items++] = (static_cast<uint32_t>(local[it.seq]) << kItemSeqShift) |
-                                   static_cast<uint32_t>(it.qt);
+                                   index(seqlens[it.seq], it.qt);
             ++pos;
         }
         for (int s : used) local[s] = -1;
@@ -176,20 +180,92 @@ bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int unit_
     }
     return true;
 }
+// Units of `unit_tokens` consecutive tokens.
+template <class Cost, class Launch>
+bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int sinks, int unit_tokens, Cost cost,
+               Launch launch) {
+    return run_plans(batch, seqlens, hkv, window, sinks, {},
+                     [=](int L) { return (L + unit_tokens - 1) / unit_tokens; }, cost,
+                     [](int, int u) { return static_cast<uint32_t>(u); }, launch);
+}
+
+// Key tiles that a q tile of T tokens visits.
+auto q_tile_cost(int T, int key_tile, int window, int sinks) {
+    return [=](int L, int qt) {
+        const int t0 = qt * T;
+        const SinkTiles st = sink_tiles((window > 0) ? std::max(0, t0 - window + 1) : 0, sinks, key_tile);
+        return st.n_sink + (std::min(L, t0 + T) - st.kv_lo + key_tile - 1) / key_tile;
+    };
+}
+
+// The plans live in host vectors: an allocation that fails is a status, not an exception
+// through the C ABI.
+template <class F>
+gdla_status_t no_throw(F &&f) {
+    try {
+        return f();
+    } catch (...) {
+        return GDLA_ERR_CUDA;
+    }
+}
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace of the backward: dH of the signal and noise heads (bf16) and the row statistics.
 struct BwdWorkspace {
-    size_t dh_sig, dh_noise, stats, total;
+    size_t dh_sig, dh_noise, stats, part, total;
 };
-BwdWorkspace bwd_workspace(long long n, int hkv) {
+BwdWorkspace bwd_workspace(long long n, int hkv, long long part_slots = 0, int sinks = 0) {
     BwdWorkspace w;
     w.dh_sig = 0;
     w.dh_noise = align256(static_cast<size_t>(n) * 4 * hkv * 128 * 2);
     w.stats = w.dh_noise + align256(static_cast<size_t>(n) * hkv * 128 * 2);
-    w.total = w.stats + align256(static_cast<size_t>(n) * hkv * kBwdStats * 4);
+    w.part = w.stats + align256(static_cast<size_t>(n) * hkv * kBwdStats * 4);
+    w.total = w.part + align256(static_cast<size_t>(part_slots) * hkv * sinks * (192 + 128) * 4);
     return w;
+}
+
+// What every prefill call checks of its lengths; *total and *longest are filled in.
+gdla_status_t check_seqlens(int batch, const int32_t *seqlens, int num_kv_heads, long long *total, int *longest) {
+    if (batch < 1 || seqlens == nullptr) return GDLA_ERR_INVALID_ARG;
+    if (num_kv_heads < 1 || num_kv_heads > GDLA_MAX_KV_HEADS) return GDLA_ERR_UNSUPPORTED;
+    long long n = 0;
+    int most = 0;
+    for (int b = 0; b < batch; ++b) {
+        if (seqlens[b] < 0) return GDLA_ERR_INVALID_ARG;
+        n += seqlens[b];
+        most = std::max(most, static_cast<int>(seqlens[b]));
+    }
+    if (n >= (1ll << 31)) return GDLA_ERR_INVALID_ARG;
+    *total = n;
+    *longest = most;
+    return GDLA_OK;
+}
+
+// Sinks count behind a window alone. A window that reaches over the longest sequence
+// is the full causal mask.
+gdla_status_t check_sinks(int longest, int *window, int *sinks) {
+    if (*sinks < 0) return GDLA_ERR_INVALID_ARG;
+    if (*sinks > GDLA_MAX_SINKS) return GDLA_ERR_UNSUPPORTED;
+    if (*sinks > 0 && *window >= longest) *window = 0;
+    if (*window <= 0) *sinks = 0;
+    // item codes carry the tile in 20 bits
+    if (*sinks > 0 && longest > (static_cast<int>(kItemTileMask) + 1) * kPrefillTileTokens) return GDLA_ERR_UNSUPPORTED;
+    return GDLA_OK;
+}
+
+// First partial slot of each sequence with sink chunks (-1: none); returns the slots in all.
+long long sink_slots(int batch, const int32_t *seqlens, int window, int sinks, std::vector<int> *part) {
+    long long slots = 0;
+    if (part) part->assign(batch, -1);
+    if (sinks <= 0) return 0;
+    for (int b = 0; b < batch; ++b) {
+        const int n = seqlens[b] > 0 ? bwd_sink_chunks(seqlens[b], window) : 0;
+        if (n == 0) continue;
+        if (part) (*part)[b] = static_cast<int>(slots);
+        slots += n + 1;
+    }
+    return slots;
 }
 
 }  // namespace
@@ -226,17 +302,14 @@ using namespace gdla;
 
 extern "C" {
 
-gdla_status_t gdla_attn_fwd(const void *q_sig, const void *q_noise, const void *k, const void *v,
-                            const float *lambda, const void *gate_logits, void *out, int batch,
-                            const int32_t *seqlens, int num_kv_heads, int window, void *stream) {
-    if (batch < 1 || seqlens == nullptr) return GDLA_ERR_INVALID_ARG;
-    if (num_kv_heads < 1 || num_kv_heads > GDLA_MAX_KV_HEADS) return GDLA_ERR_UNSUPPORTED;
+static gdla_status_t attn_fwd(const void *q_sig, const void *q_noise, const void *k, const void *v,
+                              const float *lambda, const void *gate_logits, void *out, int batch,
+                              const int32_t *seqlens, int num_kv_heads, int window, int sinks, void *stream) {
     long long n_total = 0;
-    for (int b = 0; b < batch; ++b) {
-        if (seqlens[b] < 0) return GDLA_ERR_INVALID_ARG;
-        n_total += seqlens[b];
-    }
-    if (n_total >= (1ll << 31)) return GDLA_ERR_INVALID_ARG;
+    int longest = 0;
+    gdla_status_t st = check_seqlens(batch, seqlens, num_kv_heads, &n_total, &longest);
+    if (st == GDLA_OK) st = check_sinks(longest, &window, &sinks);
+    if (st != GDLA_OK) return st;
     if (n_total == 0) return GDLA_OK;
     if (!aligned16(q_sig) || !aligned16(q_noise) || !aligned16(k) || !aligned16(v) || !aligned16(lambda) ||
         !aligned16(gate_logits) || !aligned16(out))
@@ -245,30 +318,6 @@ gdla_status_t gdla_attn_fwd(const void *q_sig, const void *q_noise, const void *
     const int hkv = num_kv_heads;
     const PrefillGeometry geo = prefill_geometry(window);
     const int T = geo.cta_tokens;
-    // ---- tile plan: every (sequence, q-tile), heaviest first ----
-    std::vector<TileItem> items;
-    std::vector<int> seq_start(batch);
-    {
-        long long s0 = 0;
-        for (int b = 0; b < batch; ++b) {
-            seq_start[b] = static_cast<int>(s0);
-            const int L = seqlens[b];
-            s0 += L;
-            const int nqt = (L + T - 1) / T;
-            for (int qt = 0; qt < nqt; ++qt) {
-                const int t0 = qt * T;
-                const int lo = (window > 0) ? std::max(0, t0 - window + 1) : 0;
-                const int hi = std::min(L, t0 + T);
-                items.push_back({(hi - lo + geo.key_tile - 1) / geo.key_tile, b, qt});
-            }
-        }
-    }
-    std::stable_sort(items.begin(), items.end(), [](const TileItem &a, const TileItem &b) {
-        if (a.cost != b.cost) return a.cost > b.cost;
-        if (a.seq != b.seq) return a.seq < b.seq;
-        return a.qt > b.qt;
-    });
-
     PrefillLaunch L{};
     const uint64_t N = static_cast<uint64_t>(n_total);
     // Q boxes: the 6 tokens one warp (TMEM lane quarter) owns in an MMA tile.
@@ -289,35 +338,31 @@ gdla_status_t gdla_attn_fwd(const void *q_sig, const void *q_noise, const void *
     L.gate = static_cast<const __nv_bfloat16 *>(gate_logits);
     L.out = static_cast<__nv_bfloat16 *>(out);
 
-    std::unique_ptr<PrefillPlan> plan(new PrefillPlan);  // filled up to n_items / n_seqs, the rest unread
-    std::vector<int> local(batch, -1);
-    size_t pos = 0;
-    while (pos < items.size()) {
-        PrefillPlan &P = *plan;
-        P.n_items = 0;
-        P.hkv = hkv;
-        P.window = window;
-        int n_seq = 0;
-        std::vector<int> used;
-        while (pos < items.size() && P.n_items < kPlanMaxItems) {
-            const TileItem &it = items[pos];
-            if (local[it.seq] < 0) {
-                if (n_seq == kPlanMaxSeqs) break;
-                local[it.seq] = n_seq;
-                P.seq_start[n_seq] = seq_start[it.seq];
-                P.seq_len[n_seq] = seqlens[it.seq];
-                used.push_back(it.seq);
-                ++n_seq;
-            }
-            P.items[P.n_items++] = (static_cast<uint32_t>(local[it.seq]) << kItemSeqShift) |
-                                   static_cast<uint32_t>(it.qt);
-            ++pos;
-        }
-        for (int s : used) local[s] = -1;
-        P.n_seqs = n_seq;
-        if (launch_prefill(L, P, static_cast<cudaStream_t>(stream)) != cudaSuccess) return GDLA_ERR_CUDA;
-    }
+    // tile plan: every (sequence, q-tile), heaviest first
+    if (!run_plans(batch, seqlens, hkv, window, sinks, T, q_tile_cost(T, geo.key_tile, window, sinks),
+                   [&](const PrefillPlan &P) {
+                       return launch_prefill(L, P, static_cast<cudaStream_t>(stream)) == cudaSuccess;
+                   }))
+        return GDLA_ERR_CUDA;
     return GDLA_OK;
+}
+
+gdla_status_t gdla_attn_fwd(const void *q_sig, const void *q_noise, const void *k, const void *v,
+                            const float *lambda, const void *gate_logits, void *out, int batch,
+                            const int32_t *seqlens, int num_kv_heads, int window, void *stream) {
+    return no_throw([&] {
+        return attn_fwd(q_sig, q_noise, k, v, lambda, gate_logits, out, batch, seqlens, num_kv_heads, window, 0,
+                        stream);
+    });
+}
+
+gdla_status_t gdla_attn_fwd_sinks(const void *q_sig, const void *q_noise, const void *k, const void *v,
+                                  const float *lambda, const void *gate_logits, void *out, int batch,
+                                  const int32_t *seqlens, int num_kv_heads, int window, int sinks, void *stream) {
+    return no_throw([&] {
+        return attn_fwd(q_sig, q_noise, k, v, lambda, gate_logits, out, batch, seqlens, num_kv_heads, window, sinks,
+                        stream);
+    });
 }
 
 size_t gdla_attn_bwd_workspace_bytes(long long total_tokens, int num_kv_heads) {
@@ -326,26 +371,25 @@ size_t gdla_attn_bwd_workspace_bytes(long long total_tokens, int num_kv_heads) {
     return bwd_workspace(total_tokens, num_kv_heads).total;
 }
 
-gdla_status_t gdla_attn_bwd(const void *q_sig, const void *q_noise, const void *k, const void *v,
+static gdla_status_t attn_bwd(const void *q_sig, const void *q_noise, const void *k, const void *v,
                             const float *lambda, const void *gate_logits, const void *dout, void *dq_sig,
                             void *dq_noise, void *dk, void *dv, float *dlambda, void *dgate, int batch,
-                            const int32_t *seqlens, int num_kv_heads, int window, void *workspace,
+                            const int32_t *seqlens, int num_kv_heads, int window, int sinks, void *workspace,
                             size_t workspace_bytes, void *stream) {
-    if (batch < 1 || seqlens == nullptr) return GDLA_ERR_INVALID_ARG;
-    if (num_kv_heads < 1 || num_kv_heads > GDLA_MAX_KV_HEADS) return GDLA_ERR_UNSUPPORTED;
     long long n_total = 0;
-    for (int b = 0; b < batch; ++b) {
-        if (seqlens[b] < 0) return GDLA_ERR_INVALID_ARG;
-        n_total += seqlens[b];
-    }
-    if (n_total >= (1ll << 31)) return GDLA_ERR_INVALID_ARG;
+    int longest = 0;
+    gdla_status_t status = check_seqlens(batch, seqlens, num_kv_heads, &n_total, &longest);
+    if (status == GDLA_OK) status = check_sinks(longest, &window, &sinks);
+    if (status != GDLA_OK) return status;
     if (n_total == 0) return GDLA_OK;
     if (!aligned16(q_sig) || !aligned16(q_noise) || !aligned16(k) || !aligned16(v) || !aligned16(lambda) ||
         !aligned16(gate_logits) || !aligned16(dout) || !aligned16(dq_sig) || !aligned16(dq_noise) ||
         !aligned16(dk) || !aligned16(dv) || !aligned16(dlambda) || !aligned16(dgate))
         return GDLA_ERR_INVALID_ARG;
     const int hkv = num_kv_heads;
-    const BwdWorkspace ws = bwd_workspace(n_total, hkv);
+    std::vector<int> part;
+    const long long slots = sink_slots(batch, seqlens, window, sinks, &part);
+    const BwdWorkspace ws = bwd_workspace(n_total, hkv, slots, sinks);
     if (workspace == nullptr || workspace_bytes < ws.total || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return GDLA_ERR_WORKSPACE;
     uint8_t *wsb = static_cast<uint8_t *>(workspace);
@@ -368,14 +412,8 @@ gdla_status_t gdla_attn_bwd(const void *q_sig, const void *q_noise, const void *
     F.gate = static_cast<const __nv_bfloat16 *>(gate_logits);
     F.bwd = {static_cast<const __nv_bfloat16 *>(dout), static_cast<__nv_bfloat16 *>(dgate), dlambda, dh_sig, dh_noise,
              stats};
-    auto q_cost = [&](int T, int key_tile) {
-        return [=](int L, int qt) {
-            const int t0 = qt * T;
-            const int lo = (window > 0) ? std::max(0, t0 - window + 1) : 0;
-            return (std::min(L, t0 + T) - lo + key_tile - 1) / key_tile;
-        };
-    };
-    if (!run_plans(batch, seqlens, hkv, window, geo.cta_tokens, q_cost(geo.cta_tokens, geo.key_tile),
+    if (!run_plans(batch, seqlens, hkv, window, sinks, geo.cta_tokens,
+                   q_tile_cost(geo.cta_tokens, geo.key_tile, window, sinks),
                    [&](const PrefillPlan &P) { return launch_prefill_bwd_recompute(F, P, st) == cudaSuccess; }))
         return GDLA_ERR_CUDA;
     const int T = kPrefillTileTokens;
@@ -400,18 +438,88 @@ gdla_status_t gdla_attn_bwd(const void *q_sig, const void *q_noise, const void *
     B.dq_noise = static_cast<__nv_bfloat16 *>(dq_noise);
     B.dk = static_cast<__nv_bfloat16 *>(dk);
     B.dv = static_cast<__nv_bfloat16 *>(dv);
-    if (!run_plans(batch, seqlens, hkv, window, T, q_cost(T, kBwdQKeyTile),
+    if (!run_plans(batch, seqlens, hkv, window, sinks, T, q_tile_cost(T, kBwdQKeyTile, window, sinks),
                    [&](const PrefillPlan &P) { return launch_bwd_dq(B, P, st) == cudaSuccess; }))
         return GDLA_ERR_CUDA;
-    auto kv_cost = [=](int L, int kt) {
-        const int u0 = kt * kBwdKeyTile;
-        const int t_end = (window > 0) ? std::min(L, u0 + kBwdKeyTile - 1 + window) : L;
-        return (t_end - u0 + kBwdStepTokens - 1) / kBwdStepTokens;
+    if (sinks == 0) {
+        auto kv_cost = [=](int L, int kt) {
+            const int u0 = kt * kBwdKeyTile;
+            const int t_end = (window > 0) ? std::min(L, u0 + kBwdKeyTile - 1 + window) : L;
+            return (t_end - u0 + kBwdStepTokens - 1) / kBwdStepTokens;
+        };
+        if (!run_plans(batch, seqlens, hkv, window, sinks, kBwdKeyTile, kv_cost,
+                       [&](const PrefillPlan &P) { return launch_bwd_dkv(B, P, st) == cudaSuccess; }))
+            return GDLA_ERR_CUDA;
+        return GDLA_OK;
+    }
+    // with sinks: the key tiles, then the chunks of later rows that see the sinks alone
+    B.part = reinterpret_cast<float *>(wsb + ws.part);
+    auto tiles = [](int L) { return (L + kBwdKeyTile - 1) / kBwdKeyTile; };
+    auto units = [=](int L) { return L > 0 ? tiles(L) + bwd_sink_chunks(L, window) : 0; };
+    auto cost = [=](int L, int u) {
+        if (u < tiles(L)) return bwd_tile_steps(L, u * kBwdKeyTile, window);
+        const int first = bwd_tile_steps(L, 0, window) + (u - tiles(L)) * kBwdSinkSteps;
+        return std::min(kBwdSinkSteps, (L + kBwdStepTokens - 1) / kBwdStepTokens - first);
     };
-    if (!run_plans(batch, seqlens, hkv, window, kBwdKeyTile, kv_cost,
+    auto index = [=](int L, int u) {
+        return u < tiles(L) ? static_cast<uint32_t>(u) : kItemSinkChunk | static_cast<uint32_t>(u - tiles(L));
+    };
+    if (!run_plans(batch, seqlens, hkv, window, sinks, part, units, cost, index,
                    [&](const PrefillPlan &P) { return launch_bwd_dkv(B, P, st) == cudaSuccess; }))
         return GDLA_ERR_CUDA;
+    std::unique_ptr<BwdSinkSum> sum(new BwdSinkSum);
+    sum->part = B.part;
+    sum->dk = B.dk;
+    sum->dv = B.dv;
+    sum->hkv = hkv;
+    sum->sinks = sinks;
+    sum->n_seqs = 0;
+    long long s0 = 0;
+    for (int b = 0; b < batch; ++b) {
+        if (part[b] >= 0) {
+            sum->start[sum->n_seqs] = static_cast<int>(s0);
+            sum->slot[sum->n_seqs] = part[b];
+            sum->count[sum->n_seqs++] = bwd_sink_chunks(seqlens[b], window) + 1;
+        }
+        s0 += seqlens[b];
+        if (sum->n_seqs > 0 && (sum->n_seqs == kSinkSumMaxSeqs || b == batch - 1)) {
+            if (launch_bwd_sink_sum(*sum, st) != cudaSuccess) return GDLA_ERR_CUDA;
+            sum->n_seqs = 0;
+        }
+    }
     return GDLA_OK;
+}
+
+size_t gdla_attn_bwd_sinks_workspace_bytes(int batch, const int32_t *seqlens, int num_kv_heads, int window,
+                                           int sinks) {
+    long long n_total = 0;
+    int longest = 0;
+    if (check_seqlens(batch, seqlens, num_kv_heads, &n_total, &longest) != GDLA_OK ||
+        check_sinks(longest, &window, &sinks) != GDLA_OK)
+        return 0;
+    return bwd_workspace(n_total, num_kv_heads, sink_slots(batch, seqlens, window, sinks, nullptr), sinks).total;
+}
+
+gdla_status_t gdla_attn_bwd(const void *q_sig, const void *q_noise, const void *k, const void *v,
+                            const float *lambda, const void *gate_logits, const void *dout, void *dq_sig,
+                            void *dq_noise, void *dk, void *dv, float *dlambda, void *dgate, int batch,
+                            const int32_t *seqlens, int num_kv_heads, int window, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    return no_throw([&] {
+        return attn_bwd(q_sig, q_noise, k, v, lambda, gate_logits, dout, dq_sig, dq_noise, dk, dv, dlambda, dgate,
+                        batch, seqlens, num_kv_heads, window, 0, workspace, workspace_bytes, stream);
+    });
+}
+
+gdla_status_t gdla_attn_bwd_sinks(const void *q_sig, const void *q_noise, const void *k, const void *v,
+                                  const float *lambda, const void *gate_logits, const void *dout, void *dq_sig,
+                                  void *dq_noise, void *dk, void *dv, float *dlambda, void *dgate, int batch,
+                                  const int32_t *seqlens, int num_kv_heads, int window, int sinks, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+    return no_throw([&] {
+        return attn_bwd(q_sig, q_noise, k, v, lambda, gate_logits, dout, dq_sig, dq_noise, dk, dv, dlambda, dgate,
+                        batch, seqlens, num_kv_heads, window, sinks, workspace, workspace_bytes, stream);
+    });
 }
 
 size_t gdla_prologue_workspace_bytes(long long total_tokens) {

@@ -36,6 +36,18 @@ __device__ __forceinline__ int snake_item(int r) {
     return r * g + ((r & 1) ? g - 1 - c : c);
 }
 
+// Key tiles of a q tile whose window starts at kv_lo, with `sinks` first tokens visible behind
+// it: the tiles that hold the sinks, then those from kv_lo on; where the two would meet,
+// one run from key 0. Every key is in one tile of the list.
+struct SinkTiles {
+    int n_sink, kv_lo;
+};
+__host__ __device__ __forceinline__ SinkTiles sink_tiles(int kv_lo, int sinks, int key_tile) {
+    const int n = (sinks + key_tile - 1) / key_tile;
+    if (kv_lo <= n * key_tile) return {0, sinks > 0 ? 0 : kv_lo};
+    return {n, kv_lo};
+}
+
 // Passed by value (kernel parameters): the q-tiles of one launch, heaviest
 // first. The host builds the largest form and launches the smallest capacity
 // that holds the plan, so a launch carries ~3.3 KB, ~8.7 KB or ~26.6 KB.
@@ -46,9 +58,11 @@ struct PrefillPlanT {
     int n_items;
     int hkv;
     int window;
+    int sinks;                // first tokens visible behind the window (0 with window <= 0)
     int n_seqs;
     int seq_start[MAX_SEQS];  // packed row of each sequence's first token
     int seq_len[MAX_SEQS];
+    int part[MAX_SEQS];       // dkv with sinks: first partial slot of the sequence, -1 for none
     uint32_t items[MAX_ITEMS];  // (local sequence << kItemSeqShift) | CTA block index
 };
 using PrefillPlan = PrefillPlanT<kPlanMaxItems, kPlanMaxSeqs>;
@@ -94,7 +108,32 @@ struct BwdLaunch {
     CUtensorMap tm_stats;           // row statistics, 12 tokens of one group
     const float *stats;
     __nv_bfloat16 *dq_sig, *dq_noise, *dk, *dv;
+    float *part;                    // sinks: fp32 partials of dK | dV, [slot][KV head][sink][320]
 };
+// dK, dV of the sinks: every later token of the sequence sees them, so the rows past the
+// first key tile's window are cut into chunks of kBwdSinkSteps steps, an item each, and
+// the items' partial sums are added up in order by a last kernel.
+constexpr int kBwdSinkSteps = 32;
+constexpr uint32_t kItemSinkChunk = 1u << 19;  // in a dkv item's tile index: sink chunk, not key tile
+// Steps of the key tile at u0, and sink chunks behind those of the first tile.
+__host__ __device__ __forceinline__ int bwd_tile_steps(int L, int u0, int window) {
+    const int t_end = (window > 0 && window < L - u0 - (kBwdKeyTile - 1)) ? u0 + kBwdKeyTile - 1 + window : L;
+    return (t_end - u0 + kBwdStepTokens - 1) / kBwdStepTokens;
+}
+__host__ __device__ __forceinline__ int bwd_sink_chunks(int L, int window) {
+    const int left = (L + kBwdStepTokens - 1) / kBwdStepTokens - bwd_tile_steps(L, 0, window);
+    return left > 0 ? (left + kBwdSinkSteps - 1) / kBwdSinkSteps : 0;
+}
+constexpr int kSinkSumMaxSeqs = 256;
+struct BwdSinkSum {  // one launch's sequences with sink chunks
+    const float *part;
+    __nv_bfloat16 *dk, *dv;
+    int hkv, sinks, n_seqs;
+    int start[kSinkSumMaxSeqs];  // packed row of the sequence's first token
+    int slot[kSinkSumMaxSeqs];   // its first partial
+    int count[kSinkSumMaxSeqs];  // its partials
+};
+cudaError_t launch_bwd_sink_sum(const BwdSinkSum &sum, cudaStream_t stream);
 cudaError_t launch_bwd_dq(const BwdLaunch &launch, const PrefillPlan &plan, cudaStream_t stream);
 cudaError_t launch_bwd_dkv(const BwdLaunch &launch, const PrefillPlan &plan, cudaStream_t stream);
 

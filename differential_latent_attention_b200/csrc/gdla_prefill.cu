@@ -106,13 +106,14 @@ enum : int {
                       // gate, lambda and H (from dout) and the row statistics
 };
 
-template <int TILES_, int BN_, int STAGES_, int EPI_>
+template <int TILES_, int BN_, int STAGES_, int EPI_, bool SINK_ = false>
 struct Cfg {
     static constexpr int TILES = TILES_;
     static constexpr int BN = BN_;          // keys per KV tile
     static constexpr int STAGES = STAGES_;
     static constexpr int V_BOX = BN;        // keys per V TMA box
     static constexpr int EPI = EPI_;
+    static constexpr bool SINK = SINK_;     // the first plan.sinks tokens stay visible behind the window
     static constexpr bool ASYNC_EPI = EPI == EPI_STAGED || EPI == EPI_HALF;  // gate / lambda staged by the producer
     static constexpr int G_HALVES = EPI == EPI_STAGED ? 2 : (EPI == EPI_HALF ? 1 : 0);
     static constexpr uint32_t GATE_TX = G_HALVES * G_HALF + LAM_TILE;
@@ -151,6 +152,8 @@ using CausalCfg = Cfg<1, 128, 2, EPI_HALF>;
 using BwdRecomputeCfg = Cfg<1, 128, 2, EPI_BWD>;         // full causal and long windows: the one-tile schedule
 using BwdRecomputeSlidingCfg = Cfg<2, 64, 2, EPI_BWD>;  // short windows: the forward's sliding schedule
 using SlidingCfg = Cfg<2, 64, 2, EPI_STAGED>;
+template <class C>
+using WithSinks = Cfg<C::TILES, C::BN, C::STAGES, C::EPI, true>;
 
 // ------------------------------- epilogue ----------------------------------
 // Per warp: the 24 signal rows of its 6 tokens. gate/out rows are 256 bytes;
@@ -378,10 +381,17 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
     // Item w: group = w % hkv, block = items[w / hkv]; key tiles of q tile x.
     struct Item {
         int group, s0, L, t0, kv_lo;
+        int n_sink;  // leading key tiles that hold the sinks (0 without sinks)
         int n_tiles[TILES];
+        // first key of key tile k
+        __device__ __forceinline__ int key0(int k) const {
+            if (C::SINK) return k < n_sink ? k * C::BN : kv_lo + (k - n_sink) * C::BN;
+            return kv_lo + k * C::BN;
+        }
     };
     auto item_at = [&](int w) {
         Item it;
+        it.n_sink = 0;
         it.group = w % hkv;
         const uint32_t code = plan.items[w / hkv];
         const int seq = static_cast<int>(code >> kItemSeqShift);
@@ -389,9 +399,14 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
         it.L = plan.seq_len[seq];
         it.t0 = static_cast<int>(code & kItemTileMask) * C::CTA_TOK;
         it.kv_lo = (window > 0) ? max(0, it.t0 - window + 1) : 0;
+        if constexpr (C::SINK) {
+            const SinkTiles st = sink_tiles(it.kv_lo, plan.sinks, BN);
+            it.n_sink = st.n_sink;
+            it.kv_lo = st.kv_lo;
+        }
 #pragma unroll
         for (int x = 0; x < TILES; ++x)
-            it.n_tiles[x] = (min(it.L, it.t0 + (x + 1) * TOK) - it.kv_lo + BN - 1) / BN;
+            it.n_tiles[x] = it.n_sink + (min(it.L, it.t0 + (x + 1) * TOK) - it.kv_lo + BN - 1) / BN;
         return it;
     };
 
@@ -495,7 +510,7 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
                 for (int k = 0; ok && k < it.n_tiles[TILES - 1]; ++k, ++kv) {
                     const int st = kv % STAGES;
                     const uint32_t use = static_cast<uint32_t>(kv / STAGES);
-                    const int row = it.s0 + it.kv_lo + k * BN;
+                    const int row = it.s0 + it.key0(k);
                     if (kv >= STAGES && !mbar_wait(k_empty + st, (use + 1) & 1, abort_flag, ERR_SITE_PREFILL | 1)) {
                         ok = false;
                         break;
@@ -678,13 +693,21 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
 #pragma unroll
                     for (int i = 0; i < 64; ++i) s[h * 64 + i] = __uint_as_float(rr[i]);
                 }
-                const int u0 = it.kv_lo + k * BN;
+                const int u0 = it.key0(k);
                 const bool need_mask = (u0 + BN - 1 > tx0) || (window > 0 && u0 < tx0 + TOK - window);
                 if (need_mask) {
                     // visible columns: keys lo_t..t of this row
                     const int c_lo = lo_t - u0, c_hi = t - u0;
+                    if constexpr (C::SINK) {
+                        // and the sinks before the window (a sink tile lies wholly before it)
+                        const int c_sink = plan.sinks - u0;
 #pragma unroll
-                    for (int i = 0; i < BN; ++i) s[i] = (i >= c_lo && i <= c_hi) ? s[i] : -INFINITY;
+                        for (int i = 0; i < BN; ++i)
+                            s[i] = (i <= c_hi && (i >= c_lo || i < c_sink)) ? s[i] : -INFINITY;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < BN; ++i) s[i] = (i >= c_lo && i <= c_hi) ? s[i] : -INFINITY;
+                    }
                 }
                 float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
 #pragma unroll
@@ -928,6 +951,7 @@ static cudaError_t launch_sized(const PrefillLaunch &L, const PrefillPlan &plan,
         small.n_items = plan.n_items;
         small.hkv = plan.hkv;
         small.window = plan.window;
+        small.sinks = plan.sinks;
         small.n_seqs = plan.n_seqs;
         std::memcpy(small.seq_start, plan.seq_start, sizeof(int) * plan.n_seqs);
         std::memcpy(small.seq_len, plan.seq_len, sizeof(int) * plan.n_seqs);
@@ -952,6 +976,10 @@ cudaError_t launch_prefill_bwd_recompute(const PrefillLaunch &L, const PrefillPl
     if (e != cudaSuccess) return e;
     const int num_sms = device_sm_count(dev);
     if (num_sms <= 0) return cudaErrorInvalidDevice;
+    if (plan.sinks > 0)
+        return plan.window <= kPrefillSlidingMaxWindow
+                   ? launch_sized<pf::WithSinks<pf::BwdRecomputeSlidingCfg>>(L, plan, dev, num_sms, stream)
+                   : launch_sized<pf::WithSinks<pf::BwdRecomputeCfg>>(L, plan, dev, num_sms, stream);
     if (plan.window > 0 && plan.window <= kPrefillSlidingMaxWindow)
         return launch_sized<pf::BwdRecomputeSlidingCfg>(L, plan, dev, num_sms, stream);
     return launch_sized<pf::BwdRecomputeCfg>(L, plan, dev, num_sms, stream);
@@ -963,6 +991,10 @@ cudaError_t launch_prefill(const PrefillLaunch &L, const PrefillPlan &plan, cuda
     if (e != cudaSuccess) return e;
     const int num_sms = device_sm_count(dev);
     if (num_sms <= 0) return cudaErrorInvalidDevice;
+    if (plan.sinks > 0)
+        return plan.window <= kPrefillSlidingMaxWindow
+                   ? launch_sized<pf::WithSinks<pf::SlidingCfg>>(L, plan, dev, num_sms, stream)
+                   : launch_sized<pf::WithSinks<LongCfg>>(L, plan, dev, num_sms, stream);
     if (plan.window > 0 && plan.window <= kPrefillSlidingMaxWindow)
         return launch_sized<pf::SlidingCfg>(L, plan, dev, num_sms, stream);
     return launch_sized<LongCfg>(L, plan, dev, num_sms, stream);

@@ -108,7 +108,7 @@ constexpr int PRODUCER_WARP = ROW_WARPS, MMA_WARP = ROW_WARPS + 1;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 }  // namespace pbq
 
-template <class Plan>
+template <class Plan, bool SINK>
 __global__ void __launch_bounds__(pbq::NUM_THREADS, 1)
 gdla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_constant__ CUtensorMap tm_qn,
                    const __grid_constant__ CUtensorMap tm_dhs, const __grid_constant__ CUtensorMap tm_dhn,
@@ -134,7 +134,11 @@ gdla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_const
     const int n_work = plan.n_items * hkv;
 
     struct Item {
-        int group, s0, L, t0, kv_lo, n_tiles;
+        int group, s0, L, t0, kv_lo, n_sink, n_tiles;
+        __device__ __forceinline__ int key0(int k) const {  // first key of key tile k
+            if (SINK) return k < n_sink ? k * pbq::BN : kv_lo + (k - n_sink) * pbq::BN;
+            return kv_lo + k * pbq::BN;
+        }
     };
     auto item_at = [&](int w) {
         Item it;
@@ -145,7 +149,13 @@ gdla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_const
         it.L = plan.seq_len[seq];
         it.t0 = static_cast<int>(code & kItemTileMask) * TOK;
         it.kv_lo = (window > 0) ? max(0, it.t0 - window + 1) : 0;
-        it.n_tiles = max(1, (min(it.L, it.t0 + TOK) - it.kv_lo + BN - 1) / BN);
+        it.n_sink = 0;
+        if constexpr (SINK) {
+            const SinkTiles st = sink_tiles(it.kv_lo, plan.sinks, BN);
+            it.n_sink = st.n_sink;
+            it.kv_lo = st.kv_lo;
+        }
+        it.n_tiles = max(1, it.n_sink + (min(it.L, it.t0 + TOK) - it.kv_lo + BN - 1) / BN);
         return it;
     };
 
@@ -215,7 +225,7 @@ gdla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_const
                         break;
                     }
                     mbar_arrive_expect_tx(kv_full + st, STAGE);
-                    const int row = it.s0 + it.kv_lo + k * BN;
+                    const int row = it.s0 + it.key0(k);
                     uint8_t *sb = smem + OFF_KV + st * STAGE;
                     for (int c = 0; c < 3; ++c) tma_load_3d(sb + c * KV_CHUNK, &tm_k, kv_full + st, c * 64, it.group, row);
                     for (int c = 0; c < 2; ++c)
@@ -336,13 +346,19 @@ gdla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_const
                 const uint32_t s_addr = lane_base + S_COL0 + b * BUF_COLS + 32 * half;
                 uint32_t sr[32], dr[32];
                 tmem_ld32x2(s_addr, lane_base + DP_COL0 + b * BUF_COLS + 32 * half, sr, dr);
-                const int u0 = it.kv_lo + k * BN + 32 * half;
+                const int u0 = it.key0(k) + 32 * half;
                 // bit c: key u0 + c is visible to this row (c <= t - u0, and c > t - window - u0)
-                const int hi = min(31, t - u0);
-                const int lo = (window > 0) ? max(0, t - window - u0 + 1) : 0;
-                const uint32_t vm = (!row_ok || hi < lo)
-                                        ? 0u
-                                        : ((hi == 31 ? 0xFFFFFFFFu : ((1u << (hi + 1)) - 1u)) & ~((1u << lo) - 1u));
+                uint32_t vm;
+                if constexpr (SINK) {  // or u0 + c is one of the sinks
+                    const auto low = [](int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); };
+                    vm = row_ok ? low(t - u0 + 1) & (~low(t - window - u0 + 1) | low(plan.sinks - u0)) : 0u;
+                } else {
+                    const int hi = min(31, t - u0);
+                    const int lo = (window > 0) ? max(0, t - window - u0 + 1) : 0;
+                    vm = (!row_ok || hi < lo)
+                             ? 0u
+                             : ((hi == 31 ? 0xFFFFFFFFu : ((1u << (hi + 1)) - 1u)) & ~((1u << lo) - 1u));
+                }
                 uint32_t pk[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -431,13 +447,13 @@ constexpr int PRODUCER_WARP = KEY_WARPS, MMA_WARP = KEY_WARPS + 1;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 }  // namespace pbk
 
-template <class Plan>
+template <class Plan, bool SINK>
 __global__ void __launch_bounds__(pbk::NUM_THREADS, 1)
 gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_constant__ CUtensorMap tm_qn,
                     const __grid_constant__ CUtensorMap tm_dhs, const __grid_constant__ CUtensorMap tm_dhn,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_stats, __nv_bfloat16 *__restrict__ dk,
-                    __nv_bfloat16 *__restrict__ dv, const __grid_constant__ Plan plan) {
+                    __nv_bfloat16 *__restrict__ dv, float *__restrict__ part, const __grid_constant__ Plan plan) {
     using namespace pbk;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -459,8 +475,11 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
 
     // Item: keys u0..u0+127 of one sequence; steps: 12-token halves from u0 to the
     // last token that sees one of the keys.
+    // With sinks: items of the first key tile's sinks over a later chunk of steps too.
     struct Item {
-        int group, s0, L, u0, n_steps;
+        int group, s0, L, u0, step0, n_steps;
+        int slot;  // partial slot of this item's sink rows, -1: every row goes straight out
+        bool chunk;
     };
     auto item_at = [&](int w) {
         Item it;
@@ -469,9 +488,27 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
         const int seq = static_cast<int>(code >> kItemSeqShift);
         it.s0 = plan.seq_start[seq];
         it.L = plan.seq_len[seq];
-        it.u0 = static_cast<int>(code & kItemTileMask) * BK;
-        const int t_end = (window > 0) ? min(it.L, it.u0 + BK - 1 + window) : it.L;
-        it.n_steps = max(1, (t_end - it.u0 + HT - 1) / HT);
+        it.step0 = 0;
+        it.slot = -1;
+        it.chunk = false;
+        if constexpr (SINK) {
+            it.chunk = (code & kItemSinkChunk) != 0;
+            it.u0 = it.chunk ? 0 : static_cast<int>(code & (kItemSinkChunk - 1)) * BK;
+            it.n_steps = bwd_tile_steps(it.L, it.u0, window);
+            if (it.chunk) {
+                const int j = static_cast<int>(code & (kItemSinkChunk - 1));
+                it.step0 = it.n_steps + j * kBwdSinkSteps;
+                it.n_steps = min(kBwdSinkSteps, (it.L + HT - 1) / HT - it.step0);
+                it.slot = plan.part[seq] + 1 + j;
+            } else if (it.u0 == 0) {
+                it.slot = plan.part[seq];
+            }
+            it.n_steps = max(1, it.n_steps);
+        } else {
+            it.u0 = static_cast<int>(code & kItemTileMask) * BK;
+            const int t_end = (window > 0) ? min(it.L, it.u0 + BK - 1 + window) : it.L;
+            it.n_steps = max(1, (t_end - it.u0 + HT - 1) / HT);
+        }
         return it;
     };
 
@@ -533,7 +570,7 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
                     }
                     mbar_arrive_expect_tx(st_full + st, STEP_TX);
                     uint8_t *sb = smem + OFF_ST + st * STAGE;
-                    const int th = it.s0 + it.u0 + s * HT;
+                    const int th = it.s0 + it.u0 + (it.step0 + s) * HT;
                     for (int c = 0; c < 3; ++c) {
                         uint8_t *dst = sb + c * H_CHUNK;
                         tma_load_3d(dst, &tm_qs, st_full + st, c * 64, 4 * it.group, th);
@@ -664,12 +701,13 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
                 mbar_arrive(dpt_free);  // dP^T is in registers: the next step's may overwrite it
                 // the step's 12 tokens: which of them see this key, and their row statistics
                 const float *stat = reinterpret_cast<const float *>(smem + OFF_ST + st * STAGE + QH_BYTES + DHH_BYTES);
-                const int th = it.u0 + s * HT;  // first token of the step
+                const int th = it.u0 + (it.step0 + s) * HT;  // first token of the step
                 uint32_t tm = 0;                // bit j: token th + j sees key u
 #pragma unroll
                 for (int j = 0; j < HT; ++j) {
                     const int t = th + j;
-                    tm |= (key_ok && u <= t && t < it.L && (window <= 0 || t < u + window)) ? (1u << j) : 0u;
+                    const bool seen = SINK ? (u < plan.sinks || t < u + window) : (window <= 0 || t < u + window);
+                    tm |= (key_ok && u <= t && t < it.L && seen) ? (1u << j) : 0u;
                 }
                 // signal rows 4j + h of the tokens j0 .. j0 + nj - 1 (h < 4), packed into pk/dk2 from 2 p0
                 auto signal_rows = [&](int j0, int nj, int r0, int p0, uint32_t (&pk)[16], uint32_t (&dk2)[16]) {
@@ -726,12 +764,26 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
             if (!__all_sync(0xffffffffu, mbar_wait(dkv_final, n_item & 1, abort_flag, ERR_SITE_BWD | 17))) break;
             tc_fence_after();
             const size_t krow = static_cast<size_t>(it.s0 + u) * hkv + it.group;
+            // sink rows of a sequence with chunks leave as fp32 partials, other rows of a chunk not at all
+            const bool to_part = SINK && it.slot >= 0 && u < plan.sinks;
+            const bool to_out = key_ok && !to_part && !(SINK && it.chunk);
+            float *prow = part;
+            if (to_part)
+                prow += ((static_cast<size_t>(it.slot) * hkv + it.group) * plan.sinks + u) * (DQK + DV);
+            const auto put_part = [&](const uint32_t (&o)[32], float f, int col) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    reinterpret_cast<float4 *>(prow + col)[i] =
+                        make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
+                                    __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
+            };
             // dK's 6 and dV's 4 32-column chunks: half 0 takes dK 0..4, half 1 dK 5 and dV 0..3
 #pragma unroll 1
             for (int ch = 5 * half; ch < (half ? DQK / 32 : 5); ++ch) {
                 uint32_t o[32];
                 tmem_ld32(lane_base + DK_COL + ch * 32, o);
-                if (key_ok) {
+                if (SINK && to_part) put_part(o, kInvRoot, ch * 32);
+                if (to_out) {
                     uint32_t wd[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -745,7 +797,8 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
             for (int ch = 0; ch < (half ? DV / 32 : 0); ++ch) {
                 uint32_t o[32];
                 tmem_ld32(lane_base + DV_COL + ch * 32, o);
-                if (key_ok) {
+                if (SINK && to_part) put_part(o, 1.f, DQK + ch * 32);
+                if (to_out) {
                     uint32_t wd[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -769,7 +822,29 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
 // ------------------------------------------------------------------------------
 // Host side
 // ------------------------------------------------------------------------------
-template <class Plan>
+// dK and dV of the sinks: the partials of a (sequence, KV head, sink) added up in slot order,
+// one thread per dim.
+__global__ void __launch_bounds__(320) gdla_bwd_sink_sum_kernel(const __grid_constant__ BwdSinkSum p) {
+    const int u = blockIdx.x % p.sinks, group = (blockIdx.x / p.sinks) % p.hkv, q = blockIdx.x / (p.sinks * p.hkv);
+    const int d = threadIdx.x;
+    const size_t step = static_cast<size_t>(p.hkv) * p.sinks * 320;
+    const float *src = p.part + (static_cast<size_t>(p.slot[q]) * p.hkv + group) * p.sinks * 320 + u * 320 + d;
+    float sum = 0.f;
+    for (int i = 0; i < p.count[q]; ++i) sum += src[i * step];
+    const size_t row = static_cast<size_t>(p.start[q] + u) * p.hkv + group;
+    if (d < 192)
+        p.dk[row * 192 + d] = __float2bfloat16_rn(sum);
+    else
+        p.dv[row * 128 + d - 192] = __float2bfloat16_rn(sum);
+}
+
+cudaError_t launch_bwd_sink_sum(const BwdSinkSum &sum, cudaStream_t stream) {
+    const unsigned grid = static_cast<unsigned>(sum.n_seqs) * sum.hkv * sum.sinks;
+    gdla_bwd_sink_sum_kernel<<<grid, 320, 0, stream>>>(sum);
+    return cudaPeekAtLastError();
+}
+
+template <bool SINK, class Plan>
 static cudaError_t launch_dq_sized(const BwdLaunch &L, const Plan &plan, cudaStream_t stream) {
     static PerContextFlag attr_set;
     int dev = 0;
@@ -779,19 +854,19 @@ static cudaError_t launch_dq_sized(const BwdLaunch &L, const Plan &plan, cudaStr
     if (num_sms <= 0) return cudaErrorInvalidDevice;
     const unsigned long long ctx = current_context_id();
     if (!attr_set.is_set(dev, ctx)) {
-        e = cudaFuncSetAttribute(gdla_bwd_dq_kernel<Plan>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(gdla_bwd_dq_kernel<Plan, SINK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  pbq::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         attr_set.set(dev, current_context_id());
     }
     const long long work = static_cast<long long>(plan.n_items) * plan.hkv;
     const unsigned grid = static_cast<unsigned>(work < num_sms ? work : num_sms);
-    gdla_bwd_dq_kernel<Plan><<<grid, pbq::NUM_THREADS, pbq::SMEM_BYTES, stream>>>(
+    gdla_bwd_dq_kernel<Plan, SINK><<<grid, pbq::NUM_THREADS, pbq::SMEM_BYTES, stream>>>(
         L.tm_qs, L.tm_qn, L.tm_dhs, L.tm_dhn, L.tm_k64, L.tm_v64, L.stats, L.dq_sig, L.dq_noise, plan);
     return cudaPeekAtLastError();
 }
 
-template <class Plan>
+template <bool SINK, class Plan>
 static cudaError_t launch_dkv_sized(const BwdLaunch &L, const Plan &plan, cudaStream_t stream) {
     static PerContextFlag attr_set;
     int dev = 0;
@@ -801,15 +876,15 @@ static cudaError_t launch_dkv_sized(const BwdLaunch &L, const Plan &plan, cudaSt
     if (num_sms <= 0) return cudaErrorInvalidDevice;
     const unsigned long long ctx = current_context_id();
     if (!attr_set.is_set(dev, ctx)) {
-        e = cudaFuncSetAttribute(gdla_bwd_dkv_kernel<Plan>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(gdla_bwd_dkv_kernel<Plan, SINK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  pbk::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         attr_set.set(dev, current_context_id());
     }
     const long long work = static_cast<long long>(plan.n_items) * plan.hkv;
     const unsigned grid = static_cast<unsigned>(work < num_sms ? work : num_sms);
-    gdla_bwd_dkv_kernel<Plan><<<grid, pbk::NUM_THREADS, pbk::SMEM_BYTES, stream>>>(
-        L.tm_qs12, L.tm_qn12, L.tm_dhs12, L.tm_dhn12, L.tm_k128, L.tm_v128, L.tm_stats, L.dk, L.dv, plan);
+    gdla_bwd_dkv_kernel<Plan, SINK><<<grid, pbk::NUM_THREADS, pbk::SMEM_BYTES, stream>>>(
+        L.tm_qs12, L.tm_qn12, L.tm_dhs12, L.tm_dhn12, L.tm_k128, L.tm_v128, L.tm_stats, L.dk, L.dv, L.part, plan);
     return cudaPeekAtLastError();
 }
 
@@ -821,9 +896,11 @@ static cudaError_t with_sized_plan(const PrefillPlan &plan, F &&launch) {
         small.n_items = plan.n_items;
         small.hkv = plan.hkv;
         small.window = plan.window;
+        small.sinks = plan.sinks;
         small.n_seqs = plan.n_seqs;
         std::memcpy(small.seq_start, plan.seq_start, sizeof(int) * plan.n_seqs);
         std::memcpy(small.seq_len, plan.seq_len, sizeof(int) * plan.n_seqs);
+        std::memcpy(small.part, plan.part, sizeof(int) * plan.n_seqs);
         std::memcpy(small.items, plan.items, sizeof(uint32_t) * plan.n_items);
     };
     if (plan.n_items <= PrefillPlanSmall::kMaxItems && plan.n_seqs <= PrefillPlanSmall::kMaxSeqs) {
@@ -840,11 +917,15 @@ static cudaError_t with_sized_plan(const PrefillPlan &plan, F &&launch) {
 }
 
 cudaError_t launch_bwd_dq(const BwdLaunch &L, const PrefillPlan &plan, cudaStream_t stream) {
-    return with_sized_plan(plan, [&](const auto &p) { return launch_dq_sized(L, p, stream); });
+    return with_sized_plan(plan, [&](const auto &p) {
+        return plan.sinks > 0 ? launch_dq_sized<true>(L, p, stream) : launch_dq_sized<false>(L, p, stream);
+    });
 }
 
 cudaError_t launch_bwd_dkv(const BwdLaunch &L, const PrefillPlan &plan, cudaStream_t stream) {
-    return with_sized_plan(plan, [&](const auto &p) { return launch_dkv_sized(L, p, stream); });
+    return with_sized_plan(plan, [&](const auto &p) {
+        return plan.sinks > 0 ? launch_dkv_sized<true>(L, p, stream) : launch_dkv_sized<false>(L, p, stream);
+    });
 }
 
 }  // namespace gdla

@@ -20,7 +20,8 @@ MAX_KV_HEADS = 64
 
 STATUS = {0: "GDLA_OK", 1: "GDLA_ERR_INVALID_ARG", 2: "GDLA_ERR_UNSUPPORTED", 3: "GDLA_ERR_WORKSPACE",
           4: "GDLA_ERR_CUDA"}
-EXPORTED = ("gdla_attn_fwd", "gdla_attn_bwd_workspace_bytes", "gdla_attn_bwd", "gdla_prologue_workspace_bytes",
+EXPORTED = ("gdla_attn_fwd", "gdla_attn_fwd_sinks", "gdla_attn_bwd_workspace_bytes", "gdla_attn_bwd",
+            "gdla_attn_bwd_sinks_workspace_bytes", "gdla_attn_bwd_sinks", "gdla_prologue_workspace_bytes",
             "gdla_prologue", "gdla_decode_workspace_bytes", "gdla_attn_decode", "gdla_attn_decode_noalloc",
             "gdla_decode_latent_workspace_bytes", "gdla_attn_decode_latent", "gdla_cache_append",
             "gdla_attn_decode_paged", "gdla_device_error",
@@ -63,6 +64,12 @@ def library():
             lib.gdla_attn_bwd_workspace_bytes.restype = sz
             lib.gdla_attn_bwd.argtypes = [p, p, p, p, p, p, p, p, p, p, p, p, p, i, p, i, i, p, sz, p]
             lib.gdla_attn_bwd.restype = i
+            lib.gdla_attn_fwd_sinks.argtypes = [p, p, p, p, p, p, p, i, p, i, i, i, p]
+            lib.gdla_attn_fwd_sinks.restype = i
+            lib.gdla_attn_bwd_sinks_workspace_bytes.argtypes = [i, p, i, i, i]
+            lib.gdla_attn_bwd_sinks_workspace_bytes.restype = sz
+            lib.gdla_attn_bwd_sinks.argtypes = [p] * 13 + [i, p, i, i, i, p, sz, p]
+            lib.gdla_attn_bwd_sinks.restype = i
             lib.gdla_prologue_workspace_bytes.argtypes = [ctypes.c_longlong]
             lib.gdla_prologue_workspace_bytes.restype = sz
             lib.gdla_prologue.argtypes = [p] * 16 + [i, p, i, p, sz, p]
@@ -147,12 +154,13 @@ def _check(t, name, dtype, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
-def attn_fwd(q_sig, q_noise, k, v, lam, gate, seqlens, window=0, out=None, stream=None):
-    """Packed varlen GDLA prefill (calls ``gdla_attn_fwd``).
+def attn_fwd(q_sig, q_noise, k, v, lam, gate, seqlens, window=0, out=None, stream=None, sinks=0):
+    """Packed varlen GDLA prefill (calls ``gdla_attn_fwd``, with sinks ``gdla_attn_fwd_sinks``).
 
     q_sig [N, 4H, 192], q_noise [N, H, 192], k [N, H, 192], v [N, H, 128] and
     gate [N, 4H, 128] are bf16 CUDA tensors, lam [N, 4H] fp32; ``seqlens`` is a
-    host sequence of per-sequence lengths summing to N. Returns out [N, 4H, 128]
+    host sequence of per-sequence lengths summing to N. With a window the first
+    ``sinks`` tokens of each sequence stay visible. Returns out [N, 4H, 128]
     bf16 (written into ``out`` when given).
     """
     lens = np.ascontiguousarray(np.asarray(seqlens, dtype=np.int32).reshape(-1))
@@ -170,11 +178,14 @@ def attn_fwd(q_sig, q_noise, k, v, lam, gate, seqlens, window=0, out=None, strea
     _check(out, "out", torch.bfloat16, (n, hs, DV))
     _on_one_device(stream, (("q_sig", q_sig), ("q_noise", q_noise), ("k", k), ("v", v), ("lam", lam),
                             ("gate", gate), ("out", out)))
-    st = library().gdla_attn_fwd(_ptr(q_sig), _ptr(q_noise), _ptr(k), _ptr(v), _ptr(lam), _ptr(gate), _ptr(out),
-                                 int(lens.shape[0]), lens.__array_interface__["data"][0], hkv, int(window),
-                                 _stream(stream))
+    args = (_ptr(q_sig), _ptr(q_noise), _ptr(k), _ptr(v), _ptr(lam), _ptr(gate), _ptr(out), int(lens.shape[0]),
+            lens.__array_interface__["data"][0], hkv, int(window))
+    if sinks:
+        st = library().gdla_attn_fwd_sinks(*args, int(sinks), _stream(stream))
+    else:
+        st = library().gdla_attn_fwd(*args, _stream(stream))
     if st != 0:
-        raise GDLAError(st, "gdla_attn_fwd")
+        raise GDLAError(st, "gdla_attn_fwd_sinks" if sinks else "gdla_attn_fwd")
     return out
 
 
@@ -182,8 +193,15 @@ def attn_bwd_workspace_bytes(total_tokens, num_kv_heads):
     return int(library().gdla_attn_bwd_workspace_bytes(int(total_tokens), int(num_kv_heads)))
 
 
-def attn_bwd(q_sig, q_noise, k, v, lam, gate, dout, seqlens, window=0, grads=None, workspace=None, stream=None):
-    """Packed varlen GDLA prefill backward (calls ``gdla_attn_bwd``).
+def attn_bwd_sinks_workspace_bytes(seqlens, num_kv_heads, window, sinks):
+    lens = np.ascontiguousarray(np.asarray(seqlens, dtype=np.int32).reshape(-1))
+    return int(library().gdla_attn_bwd_sinks_workspace_bytes(int(lens.shape[0]), lens.__array_interface__["data"][0],
+                                                             int(num_kv_heads), int(window), int(sinks)))
+
+
+def attn_bwd(q_sig, q_noise, k, v, lam, gate, dout, seqlens, window=0, grads=None, workspace=None, stream=None,
+             sinks=0):
+    """Packed varlen GDLA prefill backward (calls ``gdla_attn_bwd``, with sinks ``gdla_attn_bwd_sinks``).
 
     Inputs as ``attn_fwd`` plus dout [N, 4H, 128] bf16 (the gradient of out).
     Returns a dict of dq_sig, dq_noise, dk, dv, dgate (bf16) and dlambda (fp32),
@@ -208,20 +226,22 @@ def attn_bwd(q_sig, q_noise, k, v, lam, gate, dout, seqlens, window=0, grads=Non
         grads = {name: torch.empty(shape, dtype=dt, device=q_sig.device) for name, (shape, dt) in shapes.items()}
     for name, (shape, dt) in shapes.items():
         _check(grads[name], name, dt, shape)
-    need = attn_bwd_workspace_bytes(n, hkv)
+    need = attn_bwd_sinks_workspace_bytes(lens, hkv, window, sinks) if sinks else attn_bwd_workspace_bytes(n, hkv)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q_sig.device)
     _check_workspace(workspace)
     _on_one_device(stream, [("q_sig", q_sig), ("q_noise", q_noise), ("k", k), ("v", v), ("lam", lam),
                             ("gate", gate), ("dout", dout), ("workspace", workspace)] + list(grads.items()))
     ws_bytes = workspace.numel() * workspace.element_size()
-    st = library().gdla_attn_bwd(_ptr(q_sig), _ptr(q_noise), _ptr(k), _ptr(v), _ptr(lam), _ptr(gate), _ptr(dout),
-                                 _ptr(grads["dq_sig"]), _ptr(grads["dq_noise"]), _ptr(grads["dk"]), _ptr(grads["dv"]),
-                                 _ptr(grads["dlambda"]), _ptr(grads["dgate"]), int(lens.shape[0]),
-                                 lens.__array_interface__["data"][0], hkv, int(window), workspace.data_ptr(),
-                                 ws_bytes, _stream(stream))
+    args = (_ptr(q_sig), _ptr(q_noise), _ptr(k), _ptr(v), _ptr(lam), _ptr(gate), _ptr(dout), _ptr(grads["dq_sig"]),
+            _ptr(grads["dq_noise"]), _ptr(grads["dk"]), _ptr(grads["dv"]), _ptr(grads["dlambda"]),
+            _ptr(grads["dgate"]), int(lens.shape[0]), lens.__array_interface__["data"][0], hkv, int(window))
+    if sinks:
+        st = library().gdla_attn_bwd_sinks(*args, int(sinks), workspace.data_ptr(), ws_bytes, _stream(stream))
+    else:
+        st = library().gdla_attn_bwd(*args, workspace.data_ptr(), ws_bytes, _stream(stream))
     if st != 0:
-        raise GDLAError(st, "gdla_attn_bwd")
+        raise GDLAError(st, "gdla_attn_bwd_sinks" if sinks else "gdla_attn_bwd")
     return grads
 
 

@@ -105,6 +105,20 @@ GDLA_API gdla_status_t gdla_attn_fwd(const void *q_sig, const void *q_noise, con
                             void *stream);
 
 /*
+ * The same prefill with sinks: behind a window the first `sinks` tokens of each
+ * sequence stay visible, that is, query t sees key u <= t when t - u < window or
+ * u < sinks (a first token inside the window counts once).
+ *   sinks        0 .. GDLA_MAX_SINKS; without a window (window <= 0) it has no effect,
+ *                and sinks == 0 is gdla_attn_fwd
+ * Further errors: GDLA_ERR_INVALID_ARG for sinks < 0, GDLA_ERR_UNSUPPORTED for sinks >
+ * GDLA_MAX_SINKS or, with sinks and a window, a sequence of more than 25,165,824 tokens.
+ */
+GDLA_API gdla_status_t gdla_attn_fwd_sinks(const void *q_sig, const void *q_noise, const void *k, const void *v,
+                                           const float *lambda, const void *gate_logits, void *out, int batch,
+                                           const int32_t *seqlens, int num_kv_heads, int window, int sinks,
+                                           void *stream);
+
+/*
  * Prefill backward (the pages train GDLA end to end, aitrends.kr/articles/94908,
  * context-parallel and training-system paragraphs): the gradients of
  * sum(dout * out) for the packed varlen forward above, with the forward
@@ -131,6 +145,21 @@ GDLA_API gdla_status_t gdla_attn_bwd(const void *q_sig, const void *q_noise, con
                                      void *dq_noise, void *dk, void *dv, float *dlambda, void *dgate, int batch,
                                      const int32_t *seqlens, int num_kv_heads, int window, void *workspace,
                                      size_t workspace_bytes, void *stream);
+
+/*
+ * The backward of gdla_attn_fwd_sinks: gdla_attn_bwd with its mask. The workspace is
+ * that of gdla_attn_bwd_sinks_workspace_bytes for the same lengths, window and sinks
+ * (every token past the window adds to the sinks' dk and dv, so those rows are summed
+ * in chunks, in fp32, and joined in order). Errors as gdla_attn_bwd and gdla_attn_fwd_sinks.
+ */
+GDLA_API size_t gdla_attn_bwd_sinks_workspace_bytes(int batch, const int32_t *seqlens, int num_kv_heads, int window,
+                                                    int sinks);
+GDLA_API gdla_status_t gdla_attn_bwd_sinks(const void *q_sig, const void *q_noise, const void *k, const void *v,
+                                           const float *lambda, const void *gate_logits, const void *dout,
+                                           void *dq_sig, void *dq_noise, void *dk, void *dv, float *dlambda,
+                                           void *dgate, int batch, const int32_t *seqlens, int num_kv_heads,
+                                           int window, int sinks, void *workspace, size_t workspace_bytes,
+                                           void *stream);
 
 /*
  * Prologue: the attention's inputs from the hidden state (aitrends.kr/articles/94908,
