@@ -683,7 +683,7 @@ static gdla_status_t check_cache(const void *k_pages, const void *v_pages, const
     if (batch < 1 || num_pages < 1 || max_pages_per_seq < 1) return GDLA_ERR_INVALID_ARG;
     if (static_cast<long long>(num_pages) * num_kv_heads >= (1ll << 31) ||
         static_cast<long long>(max_pages_per_seq) * page_size >= (1ll << 31) ||
-        static_cast<long long>(batch) * num_kv_heads >= (1ll << 31))
+        static_cast<long long>(batch) * num_kv_heads >= (1ll << 24))
         return GDLA_ERR_INVALID_ARG;
     if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(block_table) || !aligned4(seqlens_k))
         return GDLA_ERR_INVALID_ARG;
@@ -737,12 +737,20 @@ gdla_status_t gdla_cache_append(const void *k_nope, long long k_nope_token_strid
     return GDLA_OK;
 }
 
+size_t gdla_decode_paged_workspace_bytes(int batch, int num_kv_heads, int max_seqlen_k, int window, int sinks) {
+    if (batch < 1 || num_kv_heads < 1 || num_kv_heads > GDLA_MAX_KV_HEADS || max_seqlen_k < 1 || sinks < 0 ||
+        sinks > GDLA_MAX_SINKS || static_cast<long long>(batch) * num_kv_heads >= (1ll << 24))
+        return 0;
+    return paged_workspace_bytes(batch, num_kv_heads,
+                                 paged_split(batch, num_kv_heads, max_seqlen_k, window, sinks));
+}
+
 gdla_status_t gdla_attn_decode_paged(const void *q_sig, const void *q_noise, const void *k_pages, const void *v_pages,
                                      const float *k_scale, const float *v_scale, int cache_type, int num_pages,
                                      int page_size, const int32_t *block_table, int max_pages_per_seq,
                                      const int32_t *seqlens_k, int max_seqlen_k, const float *lambda,
                                      const void *gate_logits, void *out, int batch, int num_kv_heads, int window,
-                                     int sinks, int rotate, void *stream) {
+                                     int sinks, int rotate, void *workspace, size_t workspace_bytes, void *stream) {
     const gdla_status_t st = check_cache(k_pages, v_pages, k_scale, v_scale, cache_type, num_pages, page_size,
                                          block_table, max_pages_per_seq, seqlens_k, batch, num_kv_heads);
     if (st != GDLA_OK) return st;
@@ -751,7 +759,16 @@ gdla_status_t gdla_attn_decode_paged(const void *q_sig, const void *q_noise, con
         return GDLA_ERR_INVALID_ARG;
     if (!aligned16(q_sig) || !aligned16(q_noise) || !aligned16(lambda) || !aligned16(gate_logits) || !aligned16(out))
         return GDLA_ERR_INVALID_ARG;
+    const PagedSplit split = paged_split(batch, num_kv_heads, max_seqlen_k, window, sinks);
+    const size_t need = paged_workspace_bytes(batch, num_kv_heads, split);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
+                     (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+        return GDLA_ERR_WORKSPACE;
     PagedDecode p{};
+    p.ws = static_cast<float *>(workspace);
+    p.splits = split.cluster * split.parts;
+    p.cluster = split.cluster;
+    p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
     p.q_sig = static_cast<const __nv_bfloat16 *>(q_sig);
     p.q_noise = static_cast<const __nv_bfloat16 *>(q_noise);
     p.k_pages = k_pages;

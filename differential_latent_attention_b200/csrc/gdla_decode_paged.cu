@@ -20,8 +20,11 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "gdla_internal.h"
 #include "gdla_paged.cuh"
+#include "gdla_pair.cuh"
 #include "gdla_ptx.cuh"
 
 namespace gdla {
@@ -29,7 +32,26 @@ namespace gdla {
 namespace dp {
 constexpr int DQK = 192, DV = 128, HEADS = 5;
 constexpr int WARPS = 4;
+constexpr int BLOCK = 16;       // keys per block
+constexpr int MAX_CLUSTER = 8;  // CTAs that join one (sequence, KV head) over distributed shared memory
 constexpr float kScoreLog2 = 0.07216878364870322f * 1.4426950408889634f;  // log2(e) / sqrt(192)
+
+template <bool E4M3>
+struct Cfg {
+    static constexpr int ELT = E4M3 ? 1 : 2;
+    static constexpr int K_BYTES = BLOCK * DQK * ELT, V_BYTES = BLOCK * DV * ELT;
+    static constexpr int STAGE = K_BYTES + V_BYTES;  // 5 or 10 KB
+    // 20 KB in flight per warp either way: 80 KB per CTA, two CTAs per SM
+    static constexpr int STAGES = E4M3 ? 4 : 2;
+    static constexpr int OFF_RED = WARPS * STAGES * STAGE;          // fp32 [WARPS][5][128]
+    static constexpr int OFF_CTA = OFF_RED + WARPS * HEADS * DV * 4;  // fp32 [5][128], this CTA's sums
+    static constexpr int OFF_ML = OFF_CTA + HEADS * DV * 4;         // fp32 [WARPS][8][2], then [8][2] of the CTA
+    static constexpr int OFF_AUX = OFF_ML + (WARPS + 1) * 8 * 2 * 4;  // float4 per stage: position, scales
+    static constexpr int OFF_BAR = OFF_AUX + WARPS * STAGES * 16;
+    static constexpr int OFF_MISC = OFF_BAR + WARPS * STAGES * 8;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16;
+    static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
+};
 }  // namespace dp
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -45,41 +67,59 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// fp32 at the address that `addr` of this CTA's shared memory has in CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(addr, rank)) : "memory");
+    return v;
+}
 
-// This lane's query fragments: head lane / 4 (zero from 5 on), for each 16-dim step the
-// dims of the MMA's K slots 2c, 2c+1 and 2c+8, 2c+9 (c = lane % 4). e4m3 keys are read four
-// codes at a time, so there slot pair s of a step is dims 4c + 2s, 4c + 2s + 1 on both sides.
-// The rotary dims 128..191 are turned to the query's position first: dim 128 + i (steps 8, 9)
-// and its partner 160 + i (steps 10, 11) sit in the same slots of one lane. Returns the
-// factor of this head's scores (1/sqrt(192) in log2 units, times the power of two taken
-// out of an f16 query).
+// The dims of a step's K slots. An MMA may take the 192 dims in any order as long as keys
+// and queries agree, so every lane reads its share of a key row in whole 16-byte units
+// straight from the page's own layout, without a swizzle: lane c = lane % 4 holds
+//   bf16: units c + 4 j (j < 6), dims 32 j + 8 c + 0..7, for steps 2 j and 2 j + 1;
+//   e4m3: units c and c + 4, dims 64 j + 16 c + 0..15, for steps 4 j .. 4 j + 3, and the 8-byte
+//         units at 128 + 8 c (steps 8, 9) and 160 + 8 c (steps 10, 11).
+// Dims i and i + 32 of the rotary part are then in one lane, two steps apart. step_dim is the
+// first of the four dims that lane c holds in a step (slots 2c, 2c+1, then 2c+8, 2c+9).
 template <bool E4M3>
-__device__ __forceinline__ float load_queries(uint32_t (&qf)[12][2], const __nv_bfloat16 *q_sig,
+__device__ __forceinline__ constexpr int step_dim(int ks, int c) {
+    if (!E4M3) return 32 * (ks >> 1) + 8 * c + 4 * (ks & 1);
+    return ks < 8 ? 64 * (ks >> 2) + 16 * c + 4 * (ks & 3) : 128 + 32 * ((ks - 8) >> 1) + 8 * c + 4 * (ks & 1);
+}
+
+// This lane's query fragments: head lane / 4 (zero from 5 on), turned to the query's position
+// where asked. bf16 keys need bf16 queries: a turned rotary part is no longer exact in
+// bf16, so its remainder goes along as a second fragment (qlo) and the scores keep fp32's
+// accuracy. e4m3 keys meet f16 queries, divided by a power of two per head. Returns the
+// factor of this head's scores.
+template <bool E4M3>
+__device__ __forceinline__ float load_queries(uint32_t (&qf)[12][2], uint32_t (&qlo)[4][2], const __nv_bfloat16 *q_sig,
                                               const __nv_bfloat16 *q_noise, size_t bg, int lane, bool rotate, int pos) {
     using namespace dp;
     const int g8 = lane >> 2, c = lane & 3;
     float x[12][4];
     const __nv_bfloat16 *row = g8 < 4 ? q_sig + (bg * 4 + g8) * DQK : q_noise + bg * DQK;
 #pragma unroll
-    for (int ks = 0; ks < 12; ++ks)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int d = 16 * ks + (E4M3 ? 4 * c + 2 * s : 2 * c + 8 * s);
-            const uint32_t two = g8 < HEADS ? *reinterpret_cast<const uint32_t *>(row + d) : 0u;
-            x[ks][2 * s] = __uint_as_float(two << 16);
-            x[ks][2 * s + 1] = __uint_as_float(two & 0xFFFF0000u);
-        }
+    for (int ks = 0; ks < 12; ++ks) {
+        const uint2 two = g8 < HEADS ? *reinterpret_cast<const uint2 *>(row + step_dim<E4M3>(ks, c)) : make_uint2(0u, 0u);
+        x[ks][0] = __uint_as_float(two.x << 16);
+        x[ks][1] = __uint_as_float(two.x & 0xFFFF0000u);
+        x[ks][2] = __uint_as_float(two.y << 16);
+        x[ks][3] = __uint_as_float(two.y & 0xFFFF0000u);
+    }
     if (rotate) {
+        float cs, sn;  // pair `lane`; the lanes share them
+        rotary_angle(pos, lane, cs, sn);
 #pragma unroll
         for (int ks = 8; ks < 10; ++ks)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = 16 * (ks - 8) + (E4M3 ? 4 * c + e : 2 * c + 8 * (e >> 1) + (e & 1));
-                float cs, sn;
-                rotary_angle(pos, i, cs, sn);
+                const int i = step_dim<E4M3>(ks, c) - 128 + e;
+                const float ci = __shfl_sync(0xffffffffu, cs, i), si = __shfl_sync(0xffffffffu, sn, i);
                 const float a = x[ks][e], b = x[ks + 2][e];
-                x[ks][e] = a * cs - b * sn;
-                x[ks + 2][e] = a * sn + b * cs;
+                x[ks][e] = a * ci - b * si;
+                x[ks + 2][e] = a * si + b * ci;
             }
     }
     float factor = kScoreLog2;
@@ -103,156 +143,423 @@ __device__ __forceinline__ float load_queries(uint32_t (&qf)[12][2], const __nv_
 #pragma unroll
         for (int ks = 0; ks < 12; ++ks)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) qf[ks][s] = pack_bf16x2(x[ks][2 * s], x[ks][2 * s + 1]);
+            for (int s = 0; s < 2; ++s) {
+                qf[ks][s] = pack_bf16x2(x[ks][2 * s], x[ks][2 * s + 1]);
+                if (ks >= 8)
+                    qlo[ks - 8][s] = pack_bf16x2(x[ks][2 * s] - __uint_as_float(qf[ks][s] << 16),
+                                                 x[ks][2 * s + 1] - __uint_as_float(qf[ks][s] & 0xFFFF0000u));
+            }
     }
     return factor;
 }
 
-// One block of four warps per (KV head, sequence); each warp takes every fourth block of
-// 16 keys, straight from global memory, and the block joins the warps at the end.
+// H = O / L per head (no key at all: zero; a NaN goes through), D = H_S - lambda H_N, the gate, bf16.
+__device__ __forceinline__ void paged_epilogue(const PagedDecode &p, size_t bg, int d, const float (&O)[dp::HEADS],
+                                               const float (&L)[dp::HEADS]) {
+    float hv[dp::HEADS];
+#pragma unroll
+    for (int h = 0; h < dp::HEADS; ++h) hv[h] = L[h] == 0.f ? 0.f : O[h] / L[h];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const size_t r = bg * 4 + i;
+        const float g = __bfloat162float(p.gate[r * dp::DV + d]);
+        p.out[r * dp::DV + d] = __float2bfloat16_rn(__fdividef(hv[i] - p.lambda[r] * hv[4], 1.f + __expf(-g)));
+    }
+}
+
+// Work: (sequence, KV head) items, each cut into `splits` runs of its visible blocks, one CTA
+// a run; `cluster` of an item's CTAs form a cluster. Inside a CTA warp w takes every fourth
+// block of the run, through a ring of its own: lane 0 copies the block's K and V rows
+// (contiguous in the page: two bulk copies) into shared memory, STAGES blocks ahead, and the
+// warp waits on nothing but its own barriers. The warps join in shared memory, the cluster's
+// CTAs in distributed shared memory; CTA 0 of the cluster applies the epilogue or, where an
+// item has several clusters, leaves its sums to the combine kernel.
 template <bool E4M3>
-__global__ void __launch_bounds__(dp::WARPS * 32)
-gdla_decode_paged_kernel(const PagedDecode p) {
+__global__ void __launch_bounds__(dp::WARPS * 32, 2)
+gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
     using namespace dp;
-    __shared__ float red[WARPS][HEADS][DV];
-    __shared__ float ml[WARPS][8][2];
-    const int group = blockIdx.x % p.hkv, b = blockIdx.x / p.hkv;
+    using C = Cfg<E4M3>;
+    extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g8 = lane >> 2, c = lane & 3;
+    const unsigned item = blockIdx.x / p.splits;
+    const int split = blockIdx.x % p.splits;
+    const int group = item % p.hkv, b = item / p.hkv;
+    const size_t bg = item;
+    uint8_t *ring = smem + warp * C::STAGES * C::STAGE;
+    float4 *aux = reinterpret_cast<float4 *>(smem + C::OFF_AUX) + warp * C::STAGES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * C::STAGES;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
+    if (lane == 0) {
+        for (int i = 0; i < C::STAGES; ++i) mbar_init(full + i, 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0) *abort_flag = 0;
+    __syncthreads();
+
     const int len = p.seqlens_k[b];
     const VisibleBlocks vis = visible_blocks(len, p.max_seqlen_k, p.window, p.sinks);
-    const size_t bg = static_cast<size_t>(b) * p.hkv + group;
+    const int i0 = static_cast<int>(static_cast<long long>(vis.n) * split / p.splits);
+    const int i1 = static_cast<int>(static_cast<long long>(vis.n) * (split + 1) / p.splits);
+    const int mine = max(0, (i1 - i0 - warp + WARPS - 1) / WARPS);  // blocks of this warp
 
-    uint32_t qf[12][2];
-    const float factor = load_queries<E4M3>(qf, p.q_sig, p.q_noise, bg, lane, p.rotate, len - 1);
+    // What a copy needs of block n of this warp, held by lane n % 32 for 32 blocks at a time and
+    // read 32 blocks ahead: page (-1: none) and scales.
+    const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_pages;
+    const auto look_up = [&](int n0, int &page, float &ks, float &vs) {
+        const int n = n0 + lane;
+        page = -1;
+        ks = vs = 1.f;
+        if (n < mine) {
+            const int id = __ldg(table + ((vis.block(i0 + warp + n * WARPS) * BLOCK) >> p.page_shift));
+            if (id >= 0 && id < p.num_pages) {
+                page = id;
+                if (E4M3) {
+                    ks = __ldg(p.k_scale + static_cast<size_t>(id) * p.hkv + group);
+                    vs = __ldg(p.v_scale + static_cast<size_t>(id) * p.hkv + group);
+                }
+            }
+        }
+    };
+    int page_cur, page_next = -1;
+    float ks_cur, vs_cur, ks_next = 1.f, vs_next = 1.f;
+    look_up(0, page_cur, ks_cur, vs_cur);
+    if (mine > 32) look_up(32, page_next, ks_next, vs_next);
+    const auto issue = [&](int n) {  // block n into its stage (the whole warp calls)
+        if (n > 0 && (n & 31) == 0) {
+            page_cur = page_next, ks_cur = ks_next, vs_cur = vs_next;
+            look_up(n + 32, page_next, ks_next, vs_next);
+        }
+        const int page = __shfl_sync(0xffffffffu, page_cur, n & 31);
+        const float ks = __shfl_sync(0xffffffffu, ks_cur, n & 31), vs = __shfl_sync(0xffffffffu, vs_cur, n & 31);
+        if (lane == 0) {
+            const int st = n % C::STAGES;
+            const int pos0 = vis.block(i0 + warp + n * WARPS) * BLOCK;
+            aux[st] = make_float4(__int_as_float(pos0), __int_as_float(page), ks, vs);
+            if (page < 0) {
+                mbar_arrive(full + st);
+            } else {
+                const size_t row = ((static_cast<size_t>(page) * p.hkv + group) << p.page_shift) +
+                                   (pos0 & (p.page_size - 1));
+                uint8_t *dst = ring + st * C::STAGE;
+                mbar_arrive_expect_tx(full + st, C::STAGE);
+                bulk_load(dst, static_cast<const uint8_t *>(p.k_pages) + row * (DQK * C::ELT), C::K_BYTES, full + st);
+                bulk_load(dst + C::K_BYTES, static_cast<const uint8_t *>(p.v_pages) + row * (DV * C::ELT), C::V_BYTES,
+                          full + st);
+            }
+        }
+    };
+    int issued = 0;
+    for (; issued < C::STAGES && issued < mine; ++issued) issue(issued);
+
+    uint32_t qf[12][2], qlo[4][2];
+    const float factor = load_queries<E4M3>(qf, qlo, p.q_sig, p.q_noise, bg, lane, p.rotate, len - 1);
+    // scores come out with heads 2c and 2c + 1 in this lane
     const float f0 = __shfl_sync(0xffffffffu, factor, (8 * c) & 31), f1 = __shfl_sync(0xffffffffu, factor, (8 * c + 4) & 31);
 
     float o[DV / 16][4];
 #pragma unroll
     for (int mt = 0; mt < DV / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2c, 2c + 1
-
-    for (int i = warp; i < vis.n; i += WARPS) {
-        const int pos0 = vis.block(i) * 16;
-        const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + pos0 / p.page_size];
-        if (page < 0 || page >= p.num_pages) continue;  // such an entry holds no keys
-        const size_t blk = static_cast<size_t>(page) * p.hkv + group;
-        const size_t row0 = blk * p.page_size + pos0 % p.page_size;
-        const float ks_ = E4M3 ? p.k_scale[blk] : 1.f, vs_ = E4M3 ? p.v_scale[blk] : 1.f;
-        const bool seen0 = vis.sees(pos0 + g8), seen1 = vis.sees(pos0 + g8 + 8);
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < 12; ++ks) {
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    bool ok = true;
+    for (int n = 0; n < mine; ++n) {
+        const int st = n % C::STAGES;
+        if (!__all_sync(0xffffffffu, mbar_wait(full + st, (n / C::STAGES) & 1, abort_flag, ERR_SITE_PAGED | 1))) {
+            ok = false;
+            break;
+        }
+        const float4 a = aux[st];
+        const int pos0 = __float_as_int(a.x);
+        if (__float_as_int(a.y) >= 0) {
+            const uint8_t *kb = ring + st * C::STAGE, *vb = kb + C::K_BYTES;
+            float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of products
             if constexpr (E4M3) {
-                const uint8_t *k = static_cast<const uint8_t *>(p.k_pages) + (row0 + g8) * DQK + 16 * ks + 4 * c;
-                const uint32_t x = *reinterpret_cast<const uint32_t *>(k);
-                const uint32_t y = *reinterpret_cast<const uint32_t *>(k + 8 * DQK);
-                mma_f16(s, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y >> 16),
-                        qf[ks][0], qf[ks][1]);
+                const uint8_t *r0 = kb + g8 * DQK, *r1 = r0 + 8 * DQK;
+                const auto step = [&](float (&d)[4], uint32_t x, uint32_t y, int ks) {
+                    mma_f16(d, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(x >> 16),
+                            e4m3x2_to_f16x2(y >> 16), qf[ks][0], qf[ks][1]);
+                };
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(r0 + 64 * j + 16 * c);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(r1 + 64 * j + 16 * c);
+                    step(s, x.x, y.x, 4 * j);
+                    step(t, x.y, y.y, 4 * j + 1);
+                    step(s, x.z, y.z, 4 * j + 2);
+                    step(t, x.w, y.w, 4 * j + 3);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(r0 + 128 + 32 * j + 8 * c);
+                    const uint2 y = *reinterpret_cast<const uint2 *>(r1 + 128 + 32 * j + 8 * c);
+                    step(s, x.x, y.x, 8 + 2 * j);
+                    step(t, x.y, y.y, 9 + 2 * j);
+                }
             } else {
-                const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(p.k_pages) + (row0 + g8) * DQK + 16 * ks + 2 * c;
-                const auto at = [&](int o_) { return *reinterpret_cast<const uint32_t *>(k + o_); };
-                mma_bf16(s, at(0), at(8 * DQK), at(8), at(8 * DQK + 8), qf[ks][0], qf[ks][1]);
+                const uint8_t *r0 = kb + g8 * (DQK * 2) + 16 * c, *r1 = r0 + 8 * DQK * 2;
+#pragma unroll
+                for (int j = 0; j < 6; ++j) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(r0 + 64 * j);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(r1 + 64 * j);
+                    mma_bf16(s, x.x, y.x, x.y, y.y, qf[2 * j][0], qf[2 * j][1]);
+                    mma_bf16(t, x.z, y.z, x.w, y.w, qf[2 * j + 1][0], qf[2 * j + 1][1]);
+                    if (j >= 4 && p.rotate) {
+                        mma_bf16(s, x.x, y.x, x.y, y.y, qlo[2 * j - 8][0], qlo[2 * j - 8][1]);
+                        mma_bf16(t, x.z, y.z, x.w, y.w, qlo[2 * j - 7][0], qlo[2 * j - 7][1]);
+                    }
+                }
+            }
+            const float k0 = f0 * a.z, k1 = f1 * a.z;
+            s[0] = (s[0] + t[0]) * k0;
+            s[1] = (s[1] + t[1]) * k1;
+            s[2] = (s[2] + t[2]) * k0;
+            s[3] = (s[3] + t[3]) * k1;
+            const bool partial = vis.partial(pos0 / BLOCK);
+            if (partial) {
+                if (!vis.sees(pos0 + g8)) s[0] = s[1] = -INFINITY;
+                if (!vis.sees(pos0 + g8 + 8)) s[2] = s[3] = -INFINITY;
+            }
+            float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+            }
+            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+            const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
+            const float a0 = fast_exp2(m0 - b0), a1 = fast_exp2(m1 - b1);
+            m0 = n0, m1 = n1;
+            const float p0 = fast_exp2(s[0] - b0), p1 = fast_exp2(s[1] - b1);
+            const float p2 = fast_exp2(s[2] - b0), p3 = fast_exp2(s[3] - b1);
+            l0 = l0 * a0 + p0 + p2;
+            l1 = l1 * a1 + p1 + p3;
+            // P^T as the second product's B operand. f16 rounds it by 2^-12; bf16's 2^-9 would show beside the
+            // output's own rounding, so there the remainder goes along as a second product.
+            uint32_t ph0, ph1, pl0 = 0u, pl1 = 0u;
+            if constexpr (E4M3) {
+                ph0 = movmatrix_t(pack_f16x2(p0, p1));
+                ph1 = movmatrix_t(pack_f16x2(p2, p3));
+            } else {
+                const uint32_t h0 = pack_bf16x2(p0, p1), h1 = pack_bf16x2(p2, p3);
+                ph0 = movmatrix_t(h0);
+                ph1 = movmatrix_t(h1);
+                pl0 = movmatrix_t(pack_bf16x2(p0 - __uint_as_float(h0 << 16), p1 - __uint_as_float(h0 & 0xFFFF0000u)));
+                pl1 = movmatrix_t(pack_bf16x2(p2 - __uint_as_float(h1 << 16), p3 - __uint_as_float(h1 & 0xFFFF0000u)));
+            }
+            // V rows of keys 2c, 2c+1, 2c+8, 2c+9, dims 16 g8 .. 16 g8 + 15: tile mt's rows g8 and g8 + 8 are
+            // dims 16 g8 + 2 mt and the next. Keys that are not seen count as zero, whatever the slot holds.
+            uint32_t v[4][4 * C::ELT];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = 2 * c + (e & 1) + 8 * (e >> 1);
+                const bool seen = !partial || vis.sees(pos0 + key);
+#pragma unroll
+                for (int w = 0; w < C::ELT; ++w) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(vb + key * (DV * C::ELT) + g8 * (16 * C::ELT) + 16 * w);
+                    v[e][4 * w] = seen ? x.x : 0u;
+                    v[e][4 * w + 1] = seen ? x.y : 0u;
+                    v[e][4 * w + 2] = seen ? x.z : 0u;
+                    v[e][4 * w + 3] = seen ? x.w : 0u;
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < DV / 16; ++mt) {
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (E4M3) {
+                    const int w = mt >> 1;
+                    const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;
+                    const uint32_t lo = __byte_perm(v[0][w], v[1][w], sel), hi = __byte_perm(v[2][w], v[3][w], sel);
+                    mma_f16(acc, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
+                            e4m3x2_to_f16x2(hi >> 16), ph0, ph1);
+                } else {
+                    const uint32_t v0 = __byte_perm(v[0][mt], v[1][mt], 0x5410), v1 = __byte_perm(v[0][mt], v[1][mt], 0x7632);
+                    const uint32_t v2 = __byte_perm(v[2][mt], v[3][mt], 0x5410), v3 = __byte_perm(v[2][mt], v[3][mt], 0x7632);
+                    mma_bf16(acc, v0, v1, v2, v3, ph0, ph1);
+                    mma_bf16(acc, v0, v1, v2, v3, pl0, pl1);
+                }
+                o[mt][0] = fmaf(o[mt][0], a0, acc[0] * a.w);
+                o[mt][1] = fmaf(o[mt][1], a1, acc[1] * a.w);
+                o[mt][2] = fmaf(o[mt][2], a0, acc[2] * a.w);
+                o[mt][3] = fmaf(o[mt][3], a1, acc[3] * a.w);
             }
         }
-        s[0] = seen0 ? s[0] * (f0 * ks_) : -INFINITY;
-        s[1] = seen0 ? s[1] * (f1 * ks_) : -INFINITY;
-        s[2] = seen1 ? s[2] * (f0 * ks_) : -INFINITY;
-        s[3] = seen1 ? s[3] * (f1 * ks_) : -INFINITY;
-        float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
-            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
-        }
-        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-        const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
-        const float a0 = fast_exp2(m0 - b0), a1 = fast_exp2(m1 - b1);
-        m0 = n0, m1 = n1;
-        const float p0 = fast_exp2(s[0] - b0), p1 = fast_exp2(s[1] - b1);
-        const float p2 = fast_exp2(s[2] - b0), p3 = fast_exp2(s[3] - b1);
-        l0 = l0 * a0 + p0 + p2;
-        l1 = l1 * a1 + p1 + p3;
-        const uint32_t pb0 = movmatrix_t(E4M3 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1));
-        const uint32_t pb1 = movmatrix_t(E4M3 ? pack_f16x2(p2, p3) : pack_bf16x2(p2, p3));
-        // values of keys that are not seen count as zero, whatever the page holds there
-        bool sv[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sv[e] = vis.sees(pos0 + 2 * c + (e & 1) + 8 * (e >> 1));
-#pragma unroll
-        for (int mt = 0; mt < DV / 16; ++mt) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (E4M3) {
-                const uint8_t *v = static_cast<const uint8_t *>(p.v_pages) + (row0 + 2 * c) * DV + 16 * mt + 2 * g8;
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = sv[e] ? *reinterpret_cast<const uint16_t *>(v + ((e & 1) + 8 * (e >> 1)) * DV) : 0u;
-                const auto two = [&](int e, int odd) {
-                    return e4m3x2_to_f16x2(((w[e] >> (8 * odd)) & 0xFFu) | (((w[e + 1] >> (8 * odd)) & 0xFFu) << 8));
-                };
-                mma_f16(acc, two(0, 0), two(0, 1), two(2, 0), two(2, 1), pb0, pb1);
-            } else {
-                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_pages) + (row0 + 2 * c) * DV + 16 * mt + g8;
-                const auto two = [&](int e, int o_) {
-                    const uint32_t lo = sv[e] ? *reinterpret_cast<const uint16_t *>(v + 4 * e * DV + o_) : 0u;
-                    const uint32_t hi = sv[e + 1] ? *reinterpret_cast<const uint16_t *>(v + (4 * e + 1) * DV + o_) : 0u;
-                    return lo | (hi << 16);
-                };
-                mma_bf16(acc, two(0, 0), two(0, 8), two(2, 0), two(2, 8), pb0, pb1);
-            }
-            o[mt][0] = fmaf(o[mt][0], a0, acc[0] * vs_);
-            o[mt][1] = fmaf(o[mt][1], a1, acc[1] * vs_);
-            o[mt][2] = fmaf(o[mt][2], a0, acc[2] * vs_);
-            o[mt][3] = fmaf(o[mt][3], a1, acc[3] * vs_);
-        }
+        // the products above have taken the stage's last values: refill it
+        __syncwarp();
+        if (issued < mine) issue(issued++);
     }
+    if (!ok) {  // a copy never came: let the others of this warp land, and leave no number behind
+        for (int n = max(0, issued - C::STAGES); n < issued; ++n)
+            mbar_wait_cycles(full + n % C::STAGES, (n / C::STAGES) & 1, 1ll << 22);
+        l0 = l1 = __uint_as_float(0x7FFFFFFFu);
+    }
+
+    float *red = reinterpret_cast<float *>(smem + C::OFF_RED), *ml = reinterpret_cast<float *>(smem + C::OFF_ML);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, off);
         l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
     if (g8 == 0) {
-        ml[warp][2 * c][0] = m0, ml[warp][2 * c][1] = l0;
-        ml[warp][2 * c + 1][0] = m1, ml[warp][2 * c + 1][1] = l1;
+        *reinterpret_cast<float4 *>(ml + (warp * 8 + 2 * c) * 2) = make_float4(m0, l0, m1, l1);
     }
-    // value dim of accumulator rows g8 and g8 + 8 of tile mt
 #pragma unroll
     for (int mt = 0; mt < DV / 16; ++mt) {
-        const int da = 16 * mt + (E4M3 ? 2 * g8 : g8), db = 16 * mt + (E4M3 ? 2 * g8 + 1 : g8 + 8);
-        if (2 * c < HEADS) red[warp][2 * c][da] = o[mt][0], red[warp][2 * c][db] = o[mt][2];
-        if (2 * c + 1 < HEADS) red[warp][2 * c + 1][da] = o[mt][1], red[warp][2 * c + 1][db] = o[mt][3];
+        const int d = 16 * g8 + 2 * mt;
+        if (2 * c < HEADS)
+            *reinterpret_cast<float2 *>(red + (warp * HEADS + 2 * c) * DV + d) = make_float2(o[mt][0], o[mt][2]);
+        if (2 * c + 1 < HEADS)
+            *reinterpret_cast<float2 *>(red + (warp * HEADS + 2 * c + 1) * DV + d) = make_float2(o[mt][1], o[mt][3]);
     }
     __syncthreads();
-    const int d = threadIdx.x;
-    float hv[HEADS];
+    const int d = threadIdx.x;  // value dim
+    float M[HEADS], L[HEADS], O[HEADS];
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h) {
+        M[h] = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) M[h] = fmaxf(M[h], ml[(w * 8 + h) * 2]);
+        L[h] = O[h] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const float mw = ml[(w * 8 + h) * 2];
+            const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M[h]);
+            L[h] += f * ml[(w * 8 + h) * 2 + 1];
+            O[h] += f * red[(w * HEADS + h) * DV + d];
+        }
+    }
+    if (p.cluster > 1) {
+        float *cta = reinterpret_cast<float *>(smem + C::OFF_CTA), *cml = ml + WARPS * 16;
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            cta[h * DV + d] = O[h];
+            if (d == h) cml[2 * h] = M[h], cml[2 * h + 1] = L[h];
+        }
+        cluster_sync();
+        if (cluster_ctarank() == 0) {
+            const uint32_t a_o = smem_u32(cta) + 4 * d, a_ml = smem_u32(cml);
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                const float own = M[h];
+                float mr[MAX_CLUSTER], lr[MAX_CLUSTER], orr[MAX_CLUSTER];
+#pragma unroll
+                for (int r = 1; r < MAX_CLUSTER; ++r) {
+                    mr[r] = -INFINITY, lr[r] = orr[r] = 0.f;
+                    if (r < p.cluster) {
+                        mr[r] = ld_cluster(a_ml + 8 * h, r);
+                        lr[r] = ld_cluster(a_ml + 8 * h + 4, r);
+                        orr[r] = ld_cluster(a_o + 4 * h * DV, r);
+                    }
+                    M[h] = fmaxf(M[h], mr[r]);
+                }
+                const float f = own == -INFINITY ? 0.f : fast_exp2(own - M[h]);
+                L[h] *= f;
+                O[h] *= f;
+#pragma unroll
+                for (int r = 1; r < MAX_CLUSTER; ++r) {
+                    const float fr = mr[r] == -INFINITY ? 0.f : fast_exp2(mr[r] - M[h]);
+                    L[h] += fr * lr[r];
+                    O[h] += fr * orr[r];
+                }
+            }
+        }
+        cluster_sync();  // the others' sums have been read: they may leave
+        if (cluster_ctarank() != 0) return;
+    }
+    const int n_part = p.splits / p.cluster;
+    if (n_part > 1) {
+        const size_t slot = static_cast<size_t>(item) * n_part + split / p.cluster;
+        float *w = p.ws + slot * (HEADS * DV);
+        float *wml = p.ws + static_cast<size_t>(p.hkv) * p.batch * n_part * (HEADS * DV) + slot * (2 * HEADS);
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            w[h * DV + d] = O[h];
+            if (d == h) wml[2 * h] = M[h], wml[2 * h + 1] = L[h];
+        }
+        return;
+    }
+    paged_epilogue(p, bg, d, O, L);
+}
+
+// Several clusters per item: their sums joined, one block of 128 threads (one per value dim) per item.
+__global__ void __launch_bounds__(dp::DV)
+gdla_decode_paged_combine_kernel(const __grid_constant__ PagedDecode p) {
+    using namespace dp;
+    const int n_part = p.splits / p.cluster, d = threadIdx.x;
+    const size_t slot0 = static_cast<size_t>(blockIdx.x) * n_part;
+    const float *wml = p.ws + static_cast<size_t>(p.hkv) * p.batch * n_part * (HEADS * DV);
+    float L[HEADS], O[HEADS];
 #pragma unroll
     for (int h = 0; h < HEADS; ++h) {
         float M = -INFINITY;
-        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, ml[w][h][0]);
-        float L = 0.f, O = 0.f;
-        for (int w = 0; w < WARPS; ++w) {
-            const float f = ml[w][h][0] == -INFINITY ? 0.f : fast_exp2(ml[w][h][0] - M);
-            L += f * ml[w][h][1];
-            O += f * red[w][h][d];
+        for (int s = 0; s < n_part; ++s) M = fmaxf(M, wml[(slot0 + s) * (2 * HEADS) + 2 * h]);
+        L[h] = O[h] = 0.f;
+        for (int s = 0; s < n_part; ++s) {
+            const float ms = wml[(slot0 + s) * (2 * HEADS) + 2 * h];
+            const float f = ms == -INFINITY ? 0.f : fast_exp2(ms - M);
+            L[h] += f * wml[(slot0 + s) * (2 * HEADS) + 2 * h + 1];
+            O[h] += f * p.ws[((slot0 + s) * HEADS + h) * DV + d];
         }
-        hv[h] = L == 0.f ? 0.f : O / L;  // no key at all: zero; a NaN goes through
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const size_t r = bg * 4 + i;
-        const float g = __bfloat162float(p.gate[r * DV + d]);
-        p.out[r * DV + d] = __float2bfloat16_rn(__fdividef(hv[i] - p.lambda[r] * hv[4], 1.f + __expf(-g)));
+    paged_epilogue(p, blockIdx.x, d, O, L);
+}
+
+// How an item is cut. Every CTA gets at least 16 blocks (four per warp) where the sizes allow
+// it: fewer and starting up and joining costs more than the copies.
+PagedSplit paged_split(int batch, int hkv, int max_seqlen_k, int window, int sinks) {
+    const long long items = static_cast<long long>(batch) * hkv;
+    const long long keys = window > 0 ? std::min<long long>(max_seqlen_k, static_cast<long long>(window) + sinks)
+                                      : max_seqlen_k;
+    const long long blocks = (keys + dp::BLOCK - 1) / dp::BLOCK;
+    const long long most = std::max<long long>(1, blocks / 16);
+    // long contexts: runs of about 1,024 keys even out unequal lengths; few items: fill the card
+    long long want = std::max(blocks / 64, (2ll * kPlanSms + items - 1) / items);
+    want = std::min(want, most);
+    PagedSplit s{1, 1};
+    while (s.cluster < dp::MAX_CLUSTER && s.cluster * 2 <= want) s.cluster *= 2;
+    if (s.cluster == dp::MAX_CLUSTER && items * dp::MAX_CLUSTER < kPlanSms * 3 / 4)
+        s.parts = static_cast<int>(std::max<long long>(1, std::min<long long>(want / dp::MAX_CLUSTER, 16)));
+    return s;
+}
+
+size_t paged_workspace_bytes(int batch, int hkv, const PagedSplit &s) {
+    return s.parts > 1 ? static_cast<size_t>(batch) * hkv * s.parts * dp::HEADS * (dp::DV + 2) * sizeof(float) : 0;
+}
+
+template <bool E4M3>
+static cudaError_t launch_decode_paged_as(const PagedDecode &p, cudaStream_t stream) {
+    static PerContextFlag attr_set;  // per device, for the context it was set in
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long ctx = current_context_id();
+    if (!attr_set.is_set(dev, ctx)) {
+        e = cudaFuncSetAttribute(gdla_decode_paged_kernel<E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 dp::Cfg<E4M3>::SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        attr_set.set(dev, current_context_id());
     }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.hkv) * p.batch * p.splits);
+    cfg.blockDim = dim3(dp::WARPS * 32);
+    cfg.dynamicSmemBytes = dp::Cfg<E4M3>::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, gdla_decode_paged_kernel<E4M3>, p);
+    if (e != cudaSuccess) return e;
+    if (p.splits > p.cluster) {
+        gdla_decode_paged_combine_kernel<<<static_cast<unsigned>(p.hkv) * p.batch, dp::DV, 0, stream>>>(p);
+        return cudaPeekAtLastError();
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_decode_paged(const PagedDecode &p, bool e4m3, cudaStream_t stream) {
-    const unsigned grid = static_cast<unsigned>(p.hkv) * static_cast<unsigned>(p.batch);
-    if (e4m3)
-        gdla_decode_paged_kernel<true><<<grid, dp::WARPS * 32, 0, stream>>>(p);
-    else
-        gdla_decode_paged_kernel<false><<<grid, dp::WARPS * 32, 0, stream>>>(p);
-    return cudaPeekAtLastError();
+    return e4m3 ? launch_decode_paged_as<true>(p, stream) : launch_decode_paged_as<false>(p, stream);
 }
 
 }  // namespace gdla

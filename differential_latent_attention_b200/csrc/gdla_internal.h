@@ -243,9 +243,17 @@ struct PagedDecode {
     const float *lambda;
     const __nv_bfloat16 *gate;
     __nv_bfloat16 *out;
-    int num_pages, page_size, max_pages, max_seqlen_k, batch, hkv, window, sinks;
+    float *ws;
+    int num_pages, page_size, page_shift, max_pages, max_seqlen_k, batch, hkv, window, sinks;
+    int splits, cluster;  // CTAs per (sequence, KV head), and how many of them form a cluster
     bool rotate;
 };
+struct PagedSplit {
+    int cluster, parts;  // CTAs per cluster, clusters per (sequence, KV head)
+};
+constexpr int kPlanSms = 148;  // SMs that the split plan counts on
+PagedSplit paged_split(int batch, int hkv, int max_seqlen_k, int window, int sinks);
+size_t paged_workspace_bytes(int batch, int hkv, const PagedSplit &split);
 cudaError_t launch_decode_paged(const PagedDecode &plan, bool e4m3, cudaStream_t stream);
 
 // Host-side decode split plan (shared by the workspace query and the launch).

@@ -24,7 +24,7 @@ EXPORTED = ("gdla_attn_fwd", "gdla_attn_fwd_sinks", "gdla_attn_bwd_workspace_byt
             "gdla_attn_bwd_sinks_workspace_bytes", "gdla_attn_bwd_sinks", "gdla_prologue_workspace_bytes",
             "gdla_prologue", "gdla_decode_workspace_bytes", "gdla_attn_decode", "gdla_attn_decode_noalloc",
             "gdla_decode_latent_workspace_bytes", "gdla_attn_decode_latent", "gdla_cache_append",
-            "gdla_attn_decode_paged", "gdla_device_error",
+            "gdla_decode_paged_workspace_bytes", "gdla_attn_decode_paged", "gdla_device_error",
             "gdla_selftest_wait_timeout", "gdla_status_string", "gdla_version")
 DC, DR = 512, 64
 DL = DC + DR
@@ -88,8 +88,10 @@ def library():
             lib.gdla_cache_append.argtypes = [p, ll, ll, p, ll, p, ll, ll, p, p, p, p, i, i, i, p, i, p, i, p, i, i, i,
                                               p]
             lib.gdla_cache_append.restype = i
-            lib.gdla_attn_decode_paged.argtypes = [p, p, p, p, p, p, i, i, i, p, i, p, i, p, p, p, i, i, i, i, i, p]
+            lib.gdla_attn_decode_paged.argtypes = [p, p, p, p, p, p, i, i, i, p, i, p, i, p, p, p, i, i, i, i, i, p, sz, p]
             lib.gdla_attn_decode_paged.restype = i
+            lib.gdla_decode_paged_workspace_bytes.argtypes = [i, i, i, i, i]
+            lib.gdla_decode_paged_workspace_bytes.restype = sz
             lib.gdla_device_error.argtypes = [i]
             lib.gdla_device_error.restype = i
             lib.gdla_selftest_wait_timeout.argtypes = [p]
@@ -461,15 +463,21 @@ def cache_append(k_nope, k_rope, v, k_pages, v_pages, block_table, cu_seqlens_ne
         raise GDLAError(st, "gdla_cache_append")
 
 
+def decode_paged_workspace_bytes(batch, num_kv_heads, max_seqlen_k, window=0, sinks=0):
+    return int(library().gdla_decode_paged_workspace_bytes(int(batch), int(num_kv_heads), int(max_seqlen_k),
+                                                           int(window), int(sinks)))
+
+
 def attn_decode_paged(q_sig, q_noise, k_pages, v_pages, block_table, seqlens_k, max_seqlen_k, lam, gate, window=0,
-                      sinks=0, k_scale=None, v_scale=None, rotate=False, out=None, stream=None):
+                      sinks=0, k_scale=None, v_scale=None, rotate=False, out=None, workspace=None, stream=None):
     """GDLA decode over a paged KV cache (calls ``gdla_attn_decode_paged``).
 
     One query per sequence, at position seqlens_k[b] - 1: q_sig [B, 4H, 192], q_noise
     [B, H, 192], lam [B, 4H], gate [B, 4H, 128] as for ``attn_decode``; the cache, its
     scales and block_table as for ``cache_append``. ``window`` > 0 keeps the last window
     keys and the first ``sinks``; ``rotate`` turns the queries' rotary dims to their
-    position first. Returns out [B, 4H, 128] bf16.
+    position first. ``workspace`` (uint8 CUDA tensor) is allocated here when not given.
+    Returns out [B, 4H, 128] bf16.
     """
     kind, np_, hkv, ps, b, width = _check_cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k)
     hs = GROUP * hkv
@@ -480,13 +488,18 @@ def attn_decode_paged(q_sig, q_noise, k_pages, v_pages, block_table, seqlens_k, 
     if out is None:
         out = torch.empty((b, hs, DV), dtype=torch.bfloat16, device=q_sig.device)
     _check(out, "out", torch.bfloat16, (b, hs, DV))
+    need = decode_paged_workspace_bytes(b, hkv, max_seqlen_k, window, sinks)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q_sig.device)
+    _check_workspace(workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _on_one_device(stream, (("q_sig", q_sig), ("q_noise", q_noise), ("k_pages", k_pages), ("v_pages", v_pages),
                             ("block_table", block_table), ("seqlens_k", seqlens_k), ("lam", lam), ("gate", gate),
-                            ("out", out), ("k_scale", k_scale), ("v_scale", v_scale)))
+                            ("out", out), ("workspace", workspace), ("k_scale", k_scale), ("v_scale", v_scale)))
     st = library().gdla_attn_decode_paged(_ptr(q_sig), _ptr(q_noise), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
                                           _ptr(v_scale), kind, np_, ps, _ptr(block_table), width, _ptr(seqlens_k),
                                           int(max_seqlen_k), _ptr(lam), _ptr(gate), _ptr(out), b, hkv, int(window),
-                                          int(sinks), 1 if rotate else 0, _stream(stream))
+                                          int(sinks), 1 if rotate else 0, _ptr(workspace), ws_bytes, _stream(stream))
     if st != 0:
         raise GDLAError(st, "gdla_attn_decode_paged")
     return out

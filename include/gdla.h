@@ -357,7 +357,7 @@ GDLA_API gdla_status_t gdla_attn_decode_noalloc(const void *q_sig, const void *q
  * page undefined. Inputs and the cache must not overlap.
  * Errors: GDLA_ERR_INVALID_ARG (null or misaligned pointers, strides, sizes < 1, an
  * unknown cache_type, num_pages * num_kv_heads or max_pages_per_seq * page_size
- * >= 2^31), GDLA_ERR_UNSUPPORTED (num_kv_heads or page_size), GDLA_ERR_CUDA.
+ * >= 2^31, batch * num_kv_heads >= 2^24), GDLA_ERR_UNSUPPORTED (num_kv_heads or page_size), GDLA_ERR_CUDA.
  */
 GDLA_API gdla_status_t gdla_cache_append(const void *k_nope, long long k_nope_token_stride,
                                          long long k_nope_head_stride, const void *k_rope,
@@ -380,15 +380,23 @@ GDLA_API gdla_status_t gdla_cache_append(const void *k_nope, long long k_nope_to
  *                position first (for queries straight from their projection)
  * Keys whose table entry is outside 0 .. num_pages-1 count as not visible. What a page
  * holds in slots that are not visible never matters, NaN included.
- * Errors as for gdla_cache_append, plus GDLA_ERR_UNSUPPORTED for sinks > GDLA_MAX_SINKS.
+ *   workspace    DEVICE scratch of gdla_decode_paged_workspace_bytes(batch, num_kv_heads,
+ *                max_seqlen_k, window, sinks) bytes, 256-byte aligned (may be NULL when that
+ *                is 0: it is needed for few sequences and heads over long contexts alone);
+ *                its contents need no initialisation
+ * Errors as for gdla_cache_append, plus GDLA_ERR_UNSUPPORTED for sinks > GDLA_MAX_SINKS and
+ * GDLA_ERR_WORKSPACE.
  */
+GDLA_API size_t gdla_decode_paged_workspace_bytes(int batch, int num_kv_heads, int max_seqlen_k, int window,
+                                                  int sinks);
 GDLA_API gdla_status_t gdla_attn_decode_paged(const void *q_sig, const void *q_noise, const void *k_pages,
                                               const void *v_pages, const float *k_scale, const float *v_scale,
                                               int cache_type, int num_pages, int page_size,
                                               const int32_t *block_table, int max_pages_per_seq,
                                               const int32_t *seqlens_k, int max_seqlen_k, const float *lambda,
                                               const void *gate_logits, void *out, int batch, int num_kv_heads,
-                                              int window, int sinks, int rotate, void *stream);
+                                              int window, int sinks, int rotate, void *workspace,
+                                              size_t workspace_bytes, void *stream);
 
 /*
  * Device-side failure word. Every wait inside the kernels is bounded (about
