@@ -31,29 +31,51 @@ namespace gdla {
 
 namespace dp {
 constexpr int DQK = 192, DV = 128, HEADS = 5;
-constexpr int WARPS = 4;
 constexpr int BLOCK = 16;       // keys per block
 constexpr int MAX_CLUSTER = 8;  // CTAs that join one (sequence, KV head) over distributed shared memory
 constexpr float kScoreLog2 = 0.07216878364870322f * 1.4426950408889634f;  // log2(e) / sqrt(192)
 
-template <bool E4M3>
+template <bool E4M3, int WARPS_>
 struct Cfg {
+    static constexpr int WARPS = WARPS_, THREADS = 32 * WARPS_;
     static constexpr int ELT = E4M3 ? 1 : 2;
     static constexpr int K_BYTES = BLOCK * DQK * ELT, V_BYTES = BLOCK * DV * ELT;
     static constexpr int STAGE = K_BYTES + V_BYTES;  // 5 or 10 KB
-    // 20 KB in flight per warp either way: 80 KB per CTA, two CTAs per SM
-    static constexpr int STAGES = E4M3 ? 4 : 2;
-    static constexpr int OFF_RED = WARPS * STAGES * STAGE;          // fp32 [WARPS][5][128]
-    static constexpr int OFF_CTA = OFF_RED + WARPS * HEADS * DV * 4;  // fp32 [5][128], this CTA's sums
-    static constexpr int OFF_ML = OFF_CTA + HEADS * DV * 4;         // fp32 [WARPS][8][2], then [8][2] of the CTA
-    static constexpr int OFF_AUX = OFF_ML + (WARPS + 1) * 8 * 2 * 4;  // float4 per stage: position, scales
-    static constexpr int OFF_BAR = OFF_AUX + WARPS * STAGES * 16;
-    static constexpr int OFF_MISC = OFF_BAR + WARPS * STAGES * 8;
-    static constexpr int SMEM_BYTES = OFF_MISC + 16;
-    static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs per SM");
+    // blocks ahead: 10 KB in flight per warp either way, 16 warps per SM
+    static constexpr int STAGES = E4M3 ? 2 : 1;
+    static constexpr int RING = WARPS * STAGES * STAGE;
+    static constexpr int RED = WARPS * HEADS * DV * 4;  // fp32 [WARPS][5][128], over the ring once it is done
+    static constexpr int OFF_CTA = RING > RED ? RING : RED;        // fp32 [5][128]: this CTA's sums, then the heads
+    static constexpr int OFF_ML = OFF_CTA + HEADS * DV * 4;        // fp32 [WARPS][8][2], then [5][2] of the CTA
+    static constexpr int OFF_AUX = OFF_ML + (WARPS + 1) * 64;      // float4 per stage: position, page, scales
+    static constexpr int SMEM_BYTES = OFF_AUX + WARPS * STAGES * 16;
+    static_assert(16 / WARPS * (SMEM_BYTES + 1024) <= 233472, "16 warps per SM");
 };
+
+// Shared-memory places of a block's rows: 16-byte units, permuted so that the eight lanes of a
+// quarter warp read eight different bank groups.
+//   K bf16 (24 units a row): units 0-3 and 4-7, 8-11 and 12-15, .. swapped in odd rows
+//   K e4m3 (12 units): as it is, the 192-byte rows already alternate
+//   V bf16 (16 units), V e4m3 (8): by the row pair (row / 2) % 4, which is the reading lane's c
+template <bool E4M3>
+__device__ __forceinline__ uint32_t k_place(int row, int unit) {
+    return E4M3 ? row * 192 + unit * 16 : row * 384 + ((unit ^ ((row & 1) << 2)) << 4);
+}
+template <bool E4M3>
+__device__ __forceinline__ uint32_t v_place(int row, int unit) {
+    const int c = (row >> 1) & 3;
+    return E4M3 ? row * 128 + ((unit ^ (c << 1)) << 4) : row * 256 + ((unit ^ ((c & 1) | ((c >> 1) << 2))) << 4);
+}
 }  // namespace dp
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile(
@@ -88,25 +110,33 @@ __device__ __forceinline__ constexpr int step_dim(int ks, int c) {
     return ks < 8 ? 64 * (ks >> 2) + 16 * c + 4 * (ks & 3) : 128 + 32 * ((ks - 8) >> 1) + 8 * c + 4 * (ks & 1);
 }
 
-// This lane's query fragments: head lane / 4 (zero from 5 on), turned to the query's position
-// where asked. bf16 keys need bf16 queries: a turned rotary part is no longer exact in
-// bf16, so its remainder goes along as a second fragment (qlo) and the scores keep fp32's
-// accuracy. e4m3 keys meet f16 queries, divided by a power of two per head. Returns the
-// factor of this head's scores.
+// This lane's queries, raw: head lane / 4 (zero from 5 on), step ks at x[ks].
 template <bool E4M3>
-__device__ __forceinline__ float load_queries(uint32_t (&qf)[12][2], uint32_t (&qlo)[4][2], const __nv_bfloat16 *q_sig,
-                                              const __nv_bfloat16 *q_noise, size_t bg, int lane, bool rotate, int pos) {
+__device__ __forceinline__ void load_queries(uint2 (&raw)[12], const __nv_bfloat16 *q_sig, const __nv_bfloat16 *q_noise,
+                                             size_t bg, int lane) {
     using namespace dp;
     const int g8 = lane >> 2, c = lane & 3;
-    float x[12][4];
     const __nv_bfloat16 *row = g8 < 4 ? q_sig + (bg * 4 + g8) * DQK : q_noise + bg * DQK;
 #pragma unroll
+    for (int ks = 0; ks < 12; ++ks)
+        raw[ks] = g8 < HEADS ? __ldg(reinterpret_cast<const uint2 *>(row + step_dim<E4M3>(ks, c))) : make_uint2(0u, 0u);
+}
+// As fragments, turned to the query's position where asked. bf16 keys need bf16 queries: a
+// turned rotary part is no longer exact in bf16, so its remainder goes along as a second
+// fragment (qlo) and the scores keep fp32's accuracy. e4m3 keys meet f16 queries, divided
+// by a power of two per head. Returns the factor of this head's scores.
+template <bool E4M3>
+__device__ __forceinline__ float query_fragments(const uint2 (&raw)[12], uint32_t (&qf)[12][2], uint32_t (&qlo)[4][2],
+                                                 int lane, bool rotate, int pos) {
+    using namespace dp;
+    const int c = lane & 3;
+    float x[12][4];
+#pragma unroll
     for (int ks = 0; ks < 12; ++ks) {
-        const uint2 two = g8 < HEADS ? *reinterpret_cast<const uint2 *>(row + step_dim<E4M3>(ks, c)) : make_uint2(0u, 0u);
-        x[ks][0] = __uint_as_float(two.x << 16);
-        x[ks][1] = __uint_as_float(two.x & 0xFFFF0000u);
-        x[ks][2] = __uint_as_float(two.y << 16);
-        x[ks][3] = __uint_as_float(two.y & 0xFFFF0000u);
+        x[ks][0] = __uint_as_float(raw[ks].x << 16);
+        x[ks][1] = __uint_as_float(raw[ks].x & 0xFFFF0000u);
+        x[ks][2] = __uint_as_float(raw[ks].y << 16);
+        x[ks][3] = __uint_as_float(raw[ks].y & 0xFFFF0000u);
     }
     if (rotate) {
         float cs, sn;  // pair `lane`; the lanes share them
@@ -153,107 +183,120 @@ __device__ __forceinline__ float load_queries(uint32_t (&qf)[12][2], uint32_t (&
     return factor;
 }
 
-// H = O / L per head (no key at all: zero; a NaN goes through), D = H_S - lambda H_N, the gate, bf16.
-__device__ __forceinline__ void paged_epilogue(const PagedDecode &p, size_t bg, int d, const float (&O)[dp::HEADS],
-                                               const float (&L)[dp::HEADS]) {
-    float hv[dp::HEADS];
-#pragma unroll
-    for (int h = 0; h < dp::HEADS; ++h) hv[h] = L[h] == 0.f ? 0.f : O[h] / L[h];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const size_t r = bg * 4 + i;
-        const float g = __bfloat162float(p.gate[r * dp::DV + d]);
-        p.out[r * dp::DV + d] = __float2bfloat16_rn(__fdividef(hv[i] - p.lambda[r] * hv[4], 1.f + __expf(-g)));
-    }
+// out = sigmoid(gate) (H_S - lambda H_N) of one value dim and signal head, in bf16.
+__device__ __forceinline__ __nv_bfloat16 paged_output(float hs, float hn, float lam, __nv_bfloat16 gate) {
+    return __float2bfloat16_rn(__fdividef(hs - lam * hn, 1.f + __expf(-__bfloat162float(gate))));
 }
+// H = O / l; no key at all: zero; a NaN goes through.
+__device__ __forceinline__ float paged_head(float O, float l) { return l == 0.f ? 0.f : O / l; }
 
 // Work: (sequence, KV head) items, each cut into `splits` runs of its visible blocks, one CTA
-// a run; `cluster` of an item's CTAs form a cluster. Inside a CTA warp w takes every fourth
-// block of the run, through a ring of its own: lane 0 copies the block's K and V rows
-// (contiguous in the page: two bulk copies) into shared memory, STAGES blocks ahead, and the
-// warp waits on nothing but its own barriers. The warps join in shared memory, the cluster's
-// CTAs in distributed shared memory; CTA 0 of the cluster applies the epilogue or, where an
-// item has several clusters, leaves its sums to the combine kernel.
-template <bool E4M3>
-__global__ void __launch_bounds__(dp::WARPS * 32, 2)
+// a run; `cluster` of an item's CTAs form a cluster. Inside a CTA warp w takes every WARPS-th
+// block of the run through a ring of its own: the lanes copy the block's K rows and V rows
+// (contiguous in the page) asynchronously, as two groups, STAGES blocks ahead, so a warp waits
+// on its own copies alone and K of the next block is under way while V of this one is
+// multiplied. The warps join in shared memory, the cluster's CTAs in distributed shared
+// memory, where CTA r finishes a share of the value dims; where an item has several clusters
+// their sums are left to the combine kernel.
+template <bool E4M3, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
 gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
     using namespace dp;
-    using C = Cfg<E4M3>;
+    using C = Cfg<E4M3, WARPS>;
+    constexpr int STAGES = C::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g8 = lane >> 2, c = lane & 3;
     const unsigned item = blockIdx.x / p.splits;
-    const int split = blockIdx.x % p.splits;
-    const int group = item % p.hkv, b = item / p.hkv;
+    const int split = blockIdx.x - item * p.splits;
+    const int b = item / p.hkv, group = item - b * p.hkv;
     const size_t bg = item;
-    uint8_t *ring = smem + warp * C::STAGES * C::STAGE;
-    float4 *aux = reinterpret_cast<float4 *>(smem + C::OFF_AUX) + warp * C::STAGES;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * C::STAGES;
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
-    if (lane == 0) {
-        for (int i = 0; i < C::STAGES; ++i) mbar_init(full + i, 1);
-        fence_mbar_init();
-    }
-    if (threadIdx.x == 0) *abort_flag = 0;
-    __syncthreads();
 
-    const int len = p.seqlens_k[b];
+    const int len = __ldg(p.seqlens_k + b);
+    uint2 q_raw[12];
+    load_queries<E4M3>(q_raw, p.q_sig, p.q_noise, bg, lane);
     const VisibleBlocks vis = visible_blocks(len, p.max_seqlen_k, p.window, p.sinks);
     const int i0 = static_cast<int>(static_cast<long long>(vis.n) * split / p.splits);
     const int i1 = static_cast<int>(static_cast<long long>(vis.n) * (split + 1) / p.splits);
     const int mine = max(0, (i1 - i0 - warp + WARPS - 1) / WARPS);  // blocks of this warp
+    const auto position = [&](int n) { return vis.block(i0 + warp + n * WARPS) * BLOCK; };
 
     // What a copy needs of block n of this warp, held by lane n % 32 for 32 blocks at a time and
-    // read 32 blocks ahead: page (-1: none) and scales.
+    // read 32 blocks ahead: page and head as one number (-1: no such page) and the scales.
     const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_pages;
-    const auto look_up = [&](int n0, int &page, float &ks, float &vs) {
+    const auto look_up = [&](int n0, int &at, float &ks, float &vs) {
         const int n = n0 + lane;
-        page = -1;
+        at = -1;
         ks = vs = 1.f;
         if (n < mine) {
-            const int id = __ldg(table + ((vis.block(i0 + warp + n * WARPS) * BLOCK) >> p.page_shift));
+            const int id = __ldg(table + (position(n) >> p.page_shift));
             if (id >= 0 && id < p.num_pages) {
-                page = id;
+                at = id * p.hkv + group;
                 if (E4M3) {
-                    ks = __ldg(p.k_scale + static_cast<size_t>(id) * p.hkv + group);
-                    vs = __ldg(p.v_scale + static_cast<size_t>(id) * p.hkv + group);
+                    ks = __ldg(p.k_scale + at);
+                    vs = __ldg(p.v_scale + at);
                 }
             }
         }
     };
-    int page_cur, page_next = -1;
+    int at_cur, at_next = -1;
     float ks_cur, vs_cur, ks_next = 1.f, vs_next = 1.f;
-    look_up(0, page_cur, ks_cur, vs_cur);
-    if (mine > 32) look_up(32, page_next, ks_next, vs_next);
-    const auto issue = [&](int n) {  // block n into its stage (the whole warp calls)
-        if (n > 0 && (n & 31) == 0) {
-            page_cur = page_next, ks_cur = ks_next, vs_cur = vs_next;
-            look_up(n + 32, page_next, ks_next, vs_next);
-        }
-        const int page = __shfl_sync(0xffffffffu, page_cur, n & 31);
-        const float ks = __shfl_sync(0xffffffffu, ks_cur, n & 31), vs = __shfl_sync(0xffffffffu, vs_cur, n & 31);
-        if (lane == 0) {
-            const int st = n % C::STAGES;
-            const int pos0 = vis.block(i0 + warp + n * WARPS) * BLOCK;
-            aux[st] = make_float4(__int_as_float(pos0), __int_as_float(page), ks, vs);
-            if (page < 0) {
-                mbar_arrive(full + st);
-            } else {
-                const size_t row = ((static_cast<size_t>(page) * p.hkv + group) << p.page_shift) +
-                                   (pos0 & (p.page_size - 1));
-                uint8_t *dst = ring + st * C::STAGE;
-                mbar_arrive_expect_tx(full + st, C::STAGE);
-                bulk_load(dst, static_cast<const uint8_t *>(p.k_pages) + row * (DQK * C::ELT), C::K_BYTES, full + st);
-                bulk_load(dst + C::K_BYTES, static_cast<const uint8_t *>(p.v_pages) + row * (DV * C::ELT), C::V_BYTES,
-                          full + st);
+    look_up(0, at_cur, ks_cur, vs_cur);
+    if (mine > 32) look_up(32, at_next, ks_next, vs_next);
+
+    uint8_t *ring = smem + warp * STAGES * C::STAGE;
+    const uint32_t ring_a = smem_u32(ring);
+    float4 *aux = reinterpret_cast<float4 *>(smem + C::OFF_AUX) + warp * STAGES;
+    // where this lane's 16-byte units of a K block go: unit 32 i + lane of the block (three units cover 4 bf16 rows)
+    uint32_t k_dst[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) k_dst[i] = k_place<E4M3>((32 * i + lane) / (12 * C::ELT), (32 * i + lane) % (12 * C::ELT));
+    const auto copy_k = [&](int n) {  // K of block n into its stage, one group (the whole warp calls)
+        if (n < mine) {
+            if (n > 0 && (n & 31) == 0) {
+                at_cur = at_next, ks_cur = ks_next, vs_cur = vs_next;
+                look_up(n + 32, at_next, ks_next, vs_next);
+            }
+            const int at = __shfl_sync(0xffffffffu, at_cur, n & 31);
+            const float ks = __shfl_sync(0xffffffffu, ks_cur, n & 31), vs = __shfl_sync(0xffffffffu, vs_cur, n & 31);
+            const int st = n % STAGES, pos0 = position(n);
+            if (lane == 0) aux[st] = make_float4(__int_as_float(pos0), __int_as_float(at), ks, vs);
+            if (at >= 0) {
+                const size_t row = (static_cast<size_t>(at) << p.page_shift) + (pos0 & (p.page_size - 1));
+                const uint8_t *src = static_cast<const uint8_t *>(p.k_pages) + row * (DQK * C::ELT) + lane * 16;
+                const uint32_t dst = ring_a + st * C::STAGE;
+#pragma unroll
+                for (int i = 0; i < C::K_BYTES / 512; ++i)
+                    cp_async16(dst + (i / 3) * 1536 + k_dst[i % 3], src + 512 * i);
             }
         }
+        cp_async_commit();
     };
-    int issued = 0;
-    for (; issued < C::STAGES && issued < mine; ++issued) issue(issued);
+    const auto copy_v = [&](int n) {  // V of block n, after copy_k(n)
+        if (n < mine) {
+            const int st = n % STAGES, pos0 = position(n);
+            const int at = __shfl_sync(0xffffffffu, at_cur, n & 31);
+            if (at >= 0) {
+                const size_t row = (static_cast<size_t>(at) << p.page_shift) + (pos0 & (p.page_size - 1));
+                const uint8_t *src = static_cast<const uint8_t *>(p.v_pages) + row * (DV * C::ELT) + lane * 16;
+                const uint32_t dst = ring_a + st * C::STAGE + C::K_BYTES;
+#pragma unroll
+                for (int i = 0; i < C::V_BYTES / 512; ++i) {
+                    const int unit = 32 * i + lane;
+                    cp_async16(dst + v_place<E4M3>(unit / (8 * C::ELT), unit % (8 * C::ELT)), src + 512 * i);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int n = 0; n < STAGES; ++n) {
+        copy_k(n);
+        copy_v(n);
+    }
 
     uint32_t qf[12][2], qlo[4][2];
-    const float factor = load_queries<E4M3>(qf, qlo, p.q_sig, p.q_noise, bg, lane, p.rotate, len - 1);
+    const float factor = query_fragments<E4M3>(q_raw, qf, qlo, lane, p.rotate, len - 1);
     // scores come out with heads 2c and 2c + 1 in this lane
     const float f0 = __shfl_sync(0xffffffffu, factor, (8 * c) & 31), f1 = __shfl_sync(0xffffffffu, factor, (8 * c + 4) & 31);
 
@@ -261,18 +304,16 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
 #pragma unroll
     for (int mt = 0; mt < DV / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    bool ok = true;
     for (int n = 0; n < mine; ++n) {
-        const int st = n % C::STAGES;
-        if (!__all_sync(0xffffffffu, mbar_wait(full + st, (n / C::STAGES) & 1, abort_flag, ERR_SITE_PAGED | 1))) {
-            ok = false;
-            break;
-        }
+        const int st = n % STAGES;
+        const uint8_t *kb = ring + st * C::STAGE, *vb = kb + C::K_BYTES;
+        cp_async_wait<2 * STAGES - 1>();  // this lane's share of K is there; behind the barrier everyone's
+        __syncwarp();
         const float4 a = aux[st];
         const int pos0 = __float_as_int(a.x);
-        if (__float_as_int(a.y) >= 0) {
-            const uint8_t *kb = ring + st * C::STAGE, *vb = kb + C::K_BYTES;
-            float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of products
+        const bool there = __float_as_int(a.y) >= 0;
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of products
+        if (there) {
             if constexpr (E4M3) {
                 const uint8_t *r0 = kb + g8 * DQK, *r1 = r0 + 8 * DQK;
                 const auto step = [&](float (&d)[4], uint32_t x, uint32_t y, int ks) {
@@ -296,11 +337,10 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
                     step(t, x.y, y.y, 9 + 2 * j);
                 }
             } else {
-                const uint8_t *r0 = kb + g8 * (DQK * 2) + 16 * c, *r1 = r0 + 8 * DQK * 2;
 #pragma unroll
                 for (int j = 0; j < 6; ++j) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(r0 + 64 * j);
-                    const uint4 y = *reinterpret_cast<const uint4 *>(r1 + 64 * j);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(kb + k_place<false>(g8, c + 4 * j));
+                    const uint4 y = *reinterpret_cast<const uint4 *>(kb + k_place<false>(g8 + 8, c + 4 * j));
                     mma_bf16(s, x.x, y.x, x.y, y.y, qf[2 * j][0], qf[2 * j][1]);
                     mma_bf16(t, x.z, y.z, x.w, y.w, qf[2 * j + 1][0], qf[2 * j + 1][1]);
                     if (j >= 4 && p.rotate) {
@@ -309,12 +349,18 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
                     }
                 }
             }
+        }
+        __syncwarp();  // every lane has its keys in registers: the stage's K may be overwritten
+        copy_k(n + STAGES);
+        float a0 = 1.f, a1 = 1.f;
+        uint32_t ph0 = 0u, ph1 = 0u, pl0 = 0u, pl1 = 0u;
+        const bool partial = vis.partial(pos0 / BLOCK);
+        if (there) {
             const float k0 = f0 * a.z, k1 = f1 * a.z;
             s[0] = (s[0] + t[0]) * k0;
             s[1] = (s[1] + t[1]) * k1;
             s[2] = (s[2] + t[2]) * k0;
             s[3] = (s[3] + t[3]) * k1;
-            const bool partial = vis.partial(pos0 / BLOCK);
             if (partial) {
                 if (!vis.sees(pos0 + g8)) s[0] = s[1] = -INFINITY;
                 if (!vis.sees(pos0 + g8 + 8)) s[2] = s[3] = -INFINITY;
@@ -327,7 +373,7 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
             }
             const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
             const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
-            const float a0 = fast_exp2(m0 - b0), a1 = fast_exp2(m1 - b1);
+            a0 = fast_exp2(m0 - b0), a1 = fast_exp2(m1 - b1);
             m0 = n0, m1 = n1;
             const float p0 = fast_exp2(s[0] - b0), p1 = fast_exp2(s[1] - b1);
             const float p2 = fast_exp2(s[2] - b0), p3 = fast_exp2(s[3] - b1);
@@ -335,7 +381,6 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
             l1 = l1 * a1 + p1 + p3;
             // P^T as the second product's B operand. f16 rounds it by 2^-12; bf16's 2^-9 would show beside the
             // output's own rounding, so there the remainder goes along as a second product.
-            uint32_t ph0, ph1, pl0 = 0u, pl1 = 0u;
             if constexpr (E4M3) {
                 ph0 = movmatrix_t(pack_f16x2(p0, p1));
                 ph1 = movmatrix_t(pack_f16x2(p2, p3));
@@ -346,62 +391,63 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
                 pl0 = movmatrix_t(pack_bf16x2(p0 - __uint_as_float(h0 << 16), p1 - __uint_as_float(h0 & 0xFFFF0000u)));
                 pl1 = movmatrix_t(pack_bf16x2(p2 - __uint_as_float(h1 << 16), p3 - __uint_as_float(h1 & 0xFFFF0000u)));
             }
+        }
+        cp_async_wait<2 * STAGES - 1>();
+        __syncwarp();
+        if (there) {
             // V rows of keys 2c, 2c+1, 2c+8, 2c+9, dims 16 g8 .. 16 g8 + 15: tile mt's rows g8 and g8 + 8 are
             // dims 16 g8 + 2 mt and the next. Keys that are not seen count as zero, whatever the slot holds.
-            uint32_t v[4][4 * C::ELT];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int key = 2 * c + (e & 1) + 8 * (e >> 1);
-                const bool seen = !partial || vis.sees(pos0 + key);
+            for (int w = 0; w < C::ELT; ++w) {
+                uint32_t v[4][4];
 #pragma unroll
-                for (int w = 0; w < C::ELT; ++w) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(vb + key * (DV * C::ELT) + g8 * (16 * C::ELT) + 16 * w);
-                    v[e][4 * w] = seen ? x.x : 0u;
-                    v[e][4 * w + 1] = seen ? x.y : 0u;
-                    v[e][4 * w + 2] = seen ? x.z : 0u;
-                    v[e][4 * w + 3] = seen ? x.w : 0u;
+                for (int e = 0; e < 4; ++e) {
+                    const int key = 2 * c + (e & 1) + 8 * (e >> 1);
+                    const bool seen = !partial || vis.sees(pos0 + key);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(vb + v_place<E4M3>(key, g8 * C::ELT + w));
+                    v[e][0] = seen ? x.x : 0u;
+                    v[e][1] = seen ? x.y : 0u;
+                    v[e][2] = seen ? x.z : 0u;
+                    v[e][3] = seen ? x.w : 0u;
                 }
-            }
 #pragma unroll
-            for (int mt = 0; mt < DV / 16; ++mt) {
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                if constexpr (E4M3) {
-                    const int w = mt >> 1;
-                    const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;
-                    const uint32_t lo = __byte_perm(v[0][w], v[1][w], sel), hi = __byte_perm(v[2][w], v[3][w], sel);
-                    mma_f16(acc, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
-                            e4m3x2_to_f16x2(hi >> 16), ph0, ph1);
-                } else {
-                    const uint32_t v0 = __byte_perm(v[0][mt], v[1][mt], 0x5410), v1 = __byte_perm(v[0][mt], v[1][mt], 0x7632);
-                    const uint32_t v2 = __byte_perm(v[2][mt], v[3][mt], 0x5410), v3 = __byte_perm(v[2][mt], v[3][mt], 0x7632);
-                    mma_bf16(acc, v0, v1, v2, v3, ph0, ph1);
-                    mma_bf16(acc, v0, v1, v2, v3, pl0, pl1);
+                for (int i = 0; i < 8 / C::ELT; ++i) {
+                    const int mt = 4 * w + i;  // (e4m3: all eight from one unit)
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    if constexpr (E4M3) {
+                        const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+                        const uint32_t lo = __byte_perm(v[0][i >> 1], v[1][i >> 1], sel);
+                        const uint32_t hi = __byte_perm(v[2][i >> 1], v[3][i >> 1], sel);
+                        mma_f16(acc, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
+                                e4m3x2_to_f16x2(hi >> 16), ph0, ph1);
+                    } else {
+                        const uint32_t v0 = __byte_perm(v[0][i], v[1][i], 0x5410), v1 = __byte_perm(v[0][i], v[1][i], 0x7632);
+                        const uint32_t v2 = __byte_perm(v[2][i], v[3][i], 0x5410), v3 = __byte_perm(v[2][i], v[3][i], 0x7632);
+                        mma_bf16(acc, v0, v1, v2, v3, ph0, ph1);
+                        mma_bf16(acc, v0, v1, v2, v3, pl0, pl1);
+                    }
+                    o[mt][0] = fmaf(o[mt][0], a0, acc[0] * a.w);
+                    o[mt][1] = fmaf(o[mt][1], a1, acc[1] * a.w);
+                    o[mt][2] = fmaf(o[mt][2], a0, acc[2] * a.w);
+                    o[mt][3] = fmaf(o[mt][3], a1, acc[3] * a.w);
                 }
-                o[mt][0] = fmaf(o[mt][0], a0, acc[0] * a.w);
-                o[mt][1] = fmaf(o[mt][1], a1, acc[1] * a.w);
-                o[mt][2] = fmaf(o[mt][2], a0, acc[2] * a.w);
-                o[mt][3] = fmaf(o[mt][3], a1, acc[3] * a.w);
             }
         }
-        // the products above have taken the stage's last values: refill it
         __syncwarp();
-        if (issued < mine) issue(issued++);
+        copy_v(n + STAGES);
     }
-    if (!ok) {  // a copy never came: let the others of this warp land, and leave no number behind
-        for (int n = max(0, issued - C::STAGES); n < issued; ++n)
-            mbar_wait_cycles(full + n % C::STAGES, (n / C::STAGES) & 1, 1ll << 22);
-        l0 = l1 = __uint_as_float(0x7FFFFFFFu);
-    }
+    cp_async_wait<0>();
 
-    float *red = reinterpret_cast<float *>(smem + C::OFF_RED), *ml = reinterpret_cast<float *>(smem + C::OFF_ML);
+    // the warps' sums over the ring
+    float *red = reinterpret_cast<float *>(smem), *ml = reinterpret_cast<float *>(smem + C::OFF_ML);
+    float *cta = reinterpret_cast<float *>(smem + C::OFF_CTA), *cml = ml + WARPS * 16;
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, off);
         l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
-    if (g8 == 0) {
-        *reinterpret_cast<float4 *>(ml + (warp * 8 + 2 * c) * 2) = make_float4(m0, l0, m1, l1);
-    }
+    if (g8 == 0) *reinterpret_cast<float4 *>(ml + (warp * 8 + 2 * c) * 2) = make_float4(m0, l0, m1, l1);
+    __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < DV / 16; ++mt) {
         const int d = 16 * g8 + 2 * mt;
@@ -411,73 +457,72 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
             *reinterpret_cast<float2 *>(red + (warp * HEADS + 2 * c + 1) * DV + d) = make_float2(o[mt][1], o[mt][3]);
     }
     __syncthreads();
-    const int d = threadIdx.x;  // value dim
-    float M[HEADS], L[HEADS], O[HEADS];
+    for (int i = threadIdx.x; i < HEADS * DV; i += C::THREADS) {
+        const int h = i / DV, d = i % DV;
+        float M = -INFINITY;
 #pragma unroll
-    for (int h = 0; h < HEADS; ++h) {
-        M[h] = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) M[h] = fmaxf(M[h], ml[(w * 8 + h) * 2]);
-        L[h] = O[h] = 0.f;
+        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, ml[(w * 8 + h) * 2]);
+        float L = 0.f, O = 0.f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
             const float mw = ml[(w * 8 + h) * 2];
-            const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M[h]);
-            L[h] += f * ml[(w * 8 + h) * 2 + 1];
-            O[h] += f * red[(w * HEADS + h) * DV + d];
+            const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+            L += f * ml[(w * 8 + h) * 2 + 1];
+            O += f * red[(w * HEADS + h) * DV + d];
         }
-    }
-    if (p.cluster > 1) {
-        float *cta = reinterpret_cast<float *>(smem + C::OFF_CTA), *cml = ml + WARPS * 16;
-#pragma unroll
-        for (int h = 0; h < HEADS; ++h) {
-            cta[h * DV + d] = O[h];
-            if (d == h) cml[2 * h] = M[h], cml[2 * h + 1] = L[h];
-        }
-        cluster_sync();
-        if (cluster_ctarank() == 0) {
-            const uint32_t a_o = smem_u32(cta) + 4 * d, a_ml = smem_u32(cml);
-#pragma unroll
-            for (int h = 0; h < HEADS; ++h) {
-                const float own = M[h];
-                float mr[MAX_CLUSTER], lr[MAX_CLUSTER], orr[MAX_CLUSTER];
-#pragma unroll
-                for (int r = 1; r < MAX_CLUSTER; ++r) {
-                    mr[r] = -INFINITY, lr[r] = orr[r] = 0.f;
-                    if (r < p.cluster) {
-                        mr[r] = ld_cluster(a_ml + 8 * h, r);
-                        lr[r] = ld_cluster(a_ml + 8 * h + 4, r);
-                        orr[r] = ld_cluster(a_o + 4 * h * DV, r);
-                    }
-                    M[h] = fmaxf(M[h], mr[r]);
-                }
-                const float f = own == -INFINITY ? 0.f : fast_exp2(own - M[h]);
-                L[h] *= f;
-                O[h] *= f;
-#pragma unroll
-                for (int r = 1; r < MAX_CLUSTER; ++r) {
-                    const float fr = mr[r] == -INFINITY ? 0.f : fast_exp2(mr[r] - M[h]);
-                    L[h] += fr * lr[r];
-                    O[h] += fr * orr[r];
-                }
-            }
-        }
-        cluster_sync();  // the others' sums have been read: they may leave
-        if (cluster_ctarank() != 0) return;
+        cta[i] = O;
+        if (d == 0) cml[2 * h] = M, cml[2 * h + 1] = L;
     }
     const int n_part = p.splits / p.cluster;
-    if (n_part > 1) {
-        const size_t slot = static_cast<size_t>(item) * n_part + split / p.cluster;
-        float *w = p.ws + slot * (HEADS * DV);
-        float *wml = p.ws + static_cast<size_t>(p.hkv) * p.batch * n_part * (HEADS * DV) + slot * (2 * HEADS);
+    if (p.cluster > 1) {
+        cluster_sync();
+        // this CTA's share of the value dims, from every CTA of the cluster
+        const int share = DV / p.cluster, d0 = cluster_ctarank() * share;
+        for (int i = threadIdx.x; i < HEADS * share; i += C::THREADS) {
+            const int h = i / share, d = d0 + i % share;
+            const uint32_t a_o = smem_u32(cta + h * DV + d), a_ml = smem_u32(cml + 2 * h);
+            float mr[MAX_CLUSTER], lr[MAX_CLUSTER], orr[MAX_CLUSTER], M = -INFINITY, L = 0.f, O = 0.f;
 #pragma unroll
-        for (int h = 0; h < HEADS; ++h) {
-            w[h * DV + d] = O[h];
-            if (d == h) wml[2 * h] = M[h], wml[2 * h + 1] = L[h];
+            for (int r = 0; r < MAX_CLUSTER; ++r) {
+                mr[r] = -INFINITY, lr[r] = orr[r] = 0.f;
+                if (r < p.cluster) {
+                    mr[r] = ld_cluster(a_ml, r);
+                    lr[r] = ld_cluster(a_ml + 4, r);
+                    orr[r] = ld_cluster(a_o, r);
+                }
+                M = fmaxf(M, mr[r]);
+            }
+#pragma unroll
+            for (int r = 0; r < MAX_CLUSTER; ++r) {
+                const float f = mr[r] == -INFINITY ? 0.f : fast_exp2(mr[r] - M);
+                L += f * lr[r];
+                O += f * orr[r];
+            }
+            if (n_part > 1) {
+                const size_t slot = static_cast<size_t>(item) * n_part + split / p.cluster;
+                p.ws[slot * (HEADS * DV) + h * DV + d] = O;
+                float *wml = p.ws + static_cast<size_t>(p.hkv) * p.batch * n_part * (HEADS * DV) + slot * (2 * HEADS);
+                if (d == 0) wml[2 * h] = M, wml[2 * h + 1] = L;
+            } else {
+                red[h * DV + d] = paged_head(O, L);
+            }
+        }
+        cluster_sync();  // everyone has read everyone's sums: the CTAs may leave
+        if (n_part > 1) return;
+        for (int i = threadIdx.x; i < 4 * share; i += C::THREADS) {
+            const int hh = i / share, dd = d0 + i % share;
+            const size_t r = bg * 4 + hh;
+            p.out[r * DV + dd] = paged_output(red[hh * DV + dd], red[4 * DV + dd], __ldg(p.lambda + r), p.gate[r * DV + dd]);
         }
         return;
     }
-    paged_epilogue(p, bg, d, O, L);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 4 * DV; i += C::THREADS) {
+        const int hh = i / DV, dd = i % DV;
+        const size_t r = bg * 4 + hh;
+        p.out[r * DV + dd] = paged_output(paged_head(cta[i], cml[2 * hh + 1]), paged_head(cta[4 * DV + dd], cml[9]),
+                                          __ldg(p.lambda + r), p.gate[r * DV + dd]);
+    }
 }
 
 // Several clusters per item: their sums joined, one block of 128 threads (one per value dim) per item.
@@ -487,20 +532,24 @@ gdla_decode_paged_combine_kernel(const __grid_constant__ PagedDecode p) {
     const int n_part = p.splits / p.cluster, d = threadIdx.x;
     const size_t slot0 = static_cast<size_t>(blockIdx.x) * n_part;
     const float *wml = p.ws + static_cast<size_t>(p.hkv) * p.batch * n_part * (HEADS * DV);
-    float L[HEADS], O[HEADS];
+    float hv[HEADS];
 #pragma unroll
     for (int h = 0; h < HEADS; ++h) {
-        float M = -INFINITY;
+        float M = -INFINITY, L = 0.f, O = 0.f;
         for (int s = 0; s < n_part; ++s) M = fmaxf(M, wml[(slot0 + s) * (2 * HEADS) + 2 * h]);
-        L[h] = O[h] = 0.f;
         for (int s = 0; s < n_part; ++s) {
             const float ms = wml[(slot0 + s) * (2 * HEADS) + 2 * h];
             const float f = ms == -INFINITY ? 0.f : fast_exp2(ms - M);
-            L[h] += f * wml[(slot0 + s) * (2 * HEADS) + 2 * h + 1];
-            O[h] += f * p.ws[((slot0 + s) * HEADS + h) * DV + d];
+            L += f * wml[(slot0 + s) * (2 * HEADS) + 2 * h + 1];
+            O += f * p.ws[((slot0 + s) * HEADS + h) * DV + d];
         }
+        hv[h] = paged_head(O, L);
     }
-    paged_epilogue(p, blockIdx.x, d, O, L);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const size_t r = static_cast<size_t>(blockIdx.x) * 4 + i;
+        p.out[r * DV + d] = paged_output(hv[i], hv[4], __ldg(p.lambda + r), p.gate[r * DV + d]);
+    }
 }
 
 // How an item is cut. Every CTA gets at least 16 blocks (four per warp) where the sizes allow
@@ -525,23 +574,24 @@ size_t paged_workspace_bytes(int batch, int hkv, const PagedSplit &s) {
     return s.parts > 1 ? static_cast<size_t>(batch) * hkv * s.parts * dp::HEADS * (dp::DV + 2) * sizeof(float) : 0;
 }
 
-template <bool E4M3>
+template <bool E4M3, int WARPS>
 static cudaError_t launch_decode_paged_as(const PagedDecode &p, cudaStream_t stream) {
+    using C = dp::Cfg<E4M3, WARPS>;
     static PerContextFlag attr_set;  // per device, for the context it was set in
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned long long ctx = current_context_id();
     if (!attr_set.is_set(dev, ctx)) {
-        e = cudaFuncSetAttribute(gdla_decode_paged_kernel<E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 dp::Cfg<E4M3>::SMEM_BYTES);
+        e = cudaFuncSetAttribute(gdla_decode_paged_kernel<E4M3, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         attr_set.set(dev, current_context_id());
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(p.hkv) * p.batch * p.splits);
-    cfg.blockDim = dim3(dp::WARPS * 32);
-    cfg.dynamicSmemBytes = dp::Cfg<E4M3>::SMEM_BYTES;
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -549,7 +599,7 @@ static cudaError_t launch_decode_paged_as(const PagedDecode &p, cudaStream_t str
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, gdla_decode_paged_kernel<E4M3>, p);
+    e = cudaLaunchKernelEx(&cfg, gdla_decode_paged_kernel<E4M3, WARPS>, p);
     if (e != cudaSuccess) return e;
     if (p.splits > p.cluster) {
         gdla_decode_paged_combine_kernel<<<static_cast<unsigned>(p.hkv) * p.batch, dp::DV, 0, stream>>>(p);
@@ -559,7 +609,9 @@ static cudaError_t launch_decode_paged_as(const PagedDecode &p, cudaStream_t str
 }
 
 cudaError_t launch_decode_paged(const PagedDecode &p, bool e4m3, cudaStream_t stream) {
-    return e4m3 ? launch_decode_paged_as<true>(p, stream) : launch_decode_paged_as<false>(p, stream);
+    const bool wide = static_cast<long long>(p.hkv) * p.batch * p.splits < 2 * kPlanSms && p.cluster > 1;
+    if (e4m3) return wide ? launch_decode_paged_as<true, 8>(p, stream) : launch_decode_paged_as<true, 4>(p, stream);
+    return wide ? launch_decode_paged_as<false, 8>(p, stream) : launch_decode_paged_as<false, 4>(p, stream);
 }
 
 }  // namespace gdla
