@@ -33,6 +33,7 @@ namespace dp {
 constexpr int DQK = 192, DV = 128, HEADS = 5;
 constexpr int BLOCK = 16;       // keys per block
 constexpr int MAX_CLUSTER = 8;  // CTAs that join one (sequence, KV head) over distributed shared memory
+constexpr float kTrail = 4.f;  // a probability is at most 2^4; with a V scale's ratio of 2^8 it stays in f16
 constexpr float kScoreLog2 = 0.07216878364870322f * 1.4426950408889634f;  // log2(e) / sqrt(192)
 
 template <bool E4M3, int WARPS_>
@@ -56,15 +57,15 @@ struct Cfg {
 // quarter warp read eight different bank groups.
 //   K bf16 (24 units a row): units 0-3 and 4-7, 8-11 and 12-15, .. swapped in odd rows
 //   K e4m3 (12 units): as it is, the 192-byte rows already alternate
-//   V bf16 (16 units), V e4m3 (8): by the row pair (row / 2) % 4, which is the reading lane's c
+//   V bf16 (16 units): by the row, for eight-row transposing matrix loads
+//   V e4m3 (8 units): by the row pair (row / 2) % 4, which is the reading lane's c
 template <bool E4M3>
 __device__ __forceinline__ uint32_t k_place(int row, int unit) {
     return E4M3 ? row * 192 + unit * 16 : row * 384 + ((unit ^ ((row & 1) << 2)) << 4);
 }
 template <bool E4M3>
 __device__ __forceinline__ uint32_t v_place(int row, int unit) {
-    const int c = (row >> 1) & 3;
-    return E4M3 ? row * 128 + ((unit ^ (c << 1)) << 4) : row * 256 + ((unit ^ ((c & 1) | ((c >> 1) << 2))) << 4);
+    return E4M3 ? row * 128 + ((unit ^ (row & 6)) << 4) : row * 256 + ((unit ^ (row & 7)) << 4);
 }
 }  // namespace dp
 
@@ -303,7 +304,14 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
     float o[DV / 16][4];
 #pragma unroll
     for (int mt = 0; mt < DV / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+    // Running maxima of heads 2c, 2c+1 (log2 units) and their sums. The maxima may trail the true ones by
+    // kTrail: then a block costs one vote, and no reduction over the keys and no rescaling.
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    // e4m3: O is held in units of vs_unit, the V scale of some page, and the probabilities take the ratio of
+    // their own page's to it, so that the products add straight onto O. Within 2^-8 .. 2^8 of it an f16
+    // probability loses nothing that its own rounding does not (at most 2^-17 of the page's scale); a page
+    // further off changes the unit.
+    float vs_unit = 1.f, vs_inv = 1.f;
     for (int n = 0; n < mine; ++n) {
         const int st = n % STAGES;
         const uint8_t *kb = ring + st * C::STAGE, *vb = kb + C::K_BYTES;
@@ -352,7 +360,6 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
         }
         __syncwarp();  // every lane has its keys in registers: the stage's K may be overwritten
         copy_k(n + STAGES);
-        float a0 = 1.f, a1 = 1.f;
         uint32_t ph0 = 0u, ph1 = 0u, pl0 = 0u, pl1 = 0u;
         const bool partial = vis.partial(pos0 / BLOCK);
         if (there) {
@@ -366,19 +373,37 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
                 if (!vis.sees(pos0 + g8 + 8)) s[2] = s[3] = -INFINITY;
             }
             float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
+            if (__any_sync(0xffffffffu, x0 > m0 + kTrail || x1 > m1 + kTrail)) {
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
-                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+                for (int off = 4; off < 32; off <<= 1) {
+                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+                }
+                const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+                const float a0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
+                const float a1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
+                m0 = n0, m1 = n1;
+                l0 *= a0, l1 *= a1;
+#pragma unroll
+                for (int mt = 0; mt < DV / 16; ++mt) o[mt][0] *= a0, o[mt][1] *= a1, o[mt][2] *= a0, o[mt][3] *= a1;
             }
-            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-            const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
-            a0 = fast_exp2(m0 - b0), a1 = fast_exp2(m1 - b1);
-            m0 = n0, m1 = n1;
-            const float p0 = fast_exp2(s[0] - b0), p1 = fast_exp2(s[1] - b1);
-            const float p2 = fast_exp2(s[2] - b0), p3 = fast_exp2(s[3] - b1);
-            l0 = l0 * a0 + p0 + p2;
-            l1 = l1 * a1 + p1 + p3;
+            const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+            float p0 = fast_exp2(s[0] - b0), p1 = fast_exp2(s[1] - b1);
+            float p2 = fast_exp2(s[2] - b0), p3 = fast_exp2(s[3] - b1);
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+            if constexpr (E4M3) {
+                float ratio = a.w * vs_inv;
+                if (!(ratio >= 0.00390625f && ratio <= 256.f) && a.w >= 1e-37f && a.w <= 1e37f) {
+                    const float f = vs_unit / a.w;
+#pragma unroll
+                    for (int mt = 0; mt < DV / 16; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[mt][e] = o[mt][e] == 0.f ? 0.f : o[mt][e] * f;
+                    vs_unit = a.w, vs_inv = 1.f / a.w, ratio = 1.f;
+                }
+                p0 *= ratio, p1 *= ratio, p2 *= ratio, p3 *= ratio;
+            }
             // P^T as the second product's B operand. f16 rounds it by 2^-12; bf16's 2^-9 would show beside the
             // output's own rounding, so there the remainder goes along as a second product.
             if constexpr (E4M3) {
@@ -395,41 +420,49 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
         cp_async_wait<2 * STAGES - 1>();
         __syncwarp();
         if (there) {
-            // V rows of keys 2c, 2c+1, 2c+8, 2c+9, dims 16 g8 .. 16 g8 + 15: tile mt's rows g8 and g8 + 8 are
-            // dims 16 g8 + 2 mt and the next. Keys that are not seen count as zero, whatever the slot holds.
-#pragma unroll
-            for (int w = 0; w < C::ELT; ++w) {
+            // V^T as the A operand; keys that are not seen count as zero, whatever the slot holds.
+            if constexpr (E4M3) {
+                // rows of keys 2c, 2c+1, 2c+8, 2c+9, dims 16 g8 .. 16 g8 + 15: rows g8 and g8 + 8 of tile mt are
+                // dims 16 g8 + 2 mt and the next
                 uint32_t v[4][4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = 2 * c + (e & 1) + 8 * (e >> 1);
-                    const bool seen = !partial || vis.sees(pos0 + key);
-                    const uint4 x = *reinterpret_cast<const uint4 *>(vb + v_place<E4M3>(key, g8 * C::ELT + w));
-                    v[e][0] = seen ? x.x : 0u;
-                    v[e][1] = seen ? x.y : 0u;
-                    v[e][2] = seen ? x.z : 0u;
-                    v[e][3] = seen ? x.w : 0u;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(vb + v_place<true>(key, g8));
+                    v[e][0] = x.x, v[e][1] = x.y, v[e][2] = x.z, v[e][3] = x.w;
+                }
+                if (partial) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!vis.sees(pos0 + 2 * c + (e & 1) + 8 * (e >> 1))) v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0u;
                 }
 #pragma unroll
-                for (int i = 0; i < 8 / C::ELT; ++i) {
-                    const int mt = 4 * w + i;  // (e4m3: all eight from one unit)
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                    if constexpr (E4M3) {
-                        const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
-                        const uint32_t lo = __byte_perm(v[0][i >> 1], v[1][i >> 1], sel);
-                        const uint32_t hi = __byte_perm(v[2][i >> 1], v[3][i >> 1], sel);
-                        mma_f16(acc, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
-                                e4m3x2_to_f16x2(hi >> 16), ph0, ph1);
-                    } else {
-                        const uint32_t v0 = __byte_perm(v[0][i], v[1][i], 0x5410), v1 = __byte_perm(v[0][i], v[1][i], 0x7632);
-                        const uint32_t v2 = __byte_perm(v[2][i], v[3][i], 0x5410), v3 = __byte_perm(v[2][i], v[3][i], 0x7632);
-                        mma_bf16(acc, v0, v1, v2, v3, ph0, ph1);
-                        mma_bf16(acc, v0, v1, v2, v3, pl0, pl1);
-                    }
-                    o[mt][0] = fmaf(o[mt][0], a0, acc[0] * a.w);
-                    o[mt][1] = fmaf(o[mt][1], a1, acc[1] * a.w);
-                    o[mt][2] = fmaf(o[mt][2], a0, acc[2] * a.w);
-                    o[mt][3] = fmaf(o[mt][3], a1, acc[3] * a.w);
+                for (int mt = 0; mt < DV / 16; ++mt) {
+                    const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;
+                    const uint32_t lo = __byte_perm(v[0][mt >> 1], v[1][mt >> 1], sel);
+                    const uint32_t hi = __byte_perm(v[2][mt >> 1], v[3][mt >> 1], sel);
+                    mma_f16(o[mt], e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
+                            e4m3x2_to_f16x2(hi >> 16), ph0, ph1);
+                }
+            } else {
+                // matrices (keys 0-7 | 8-15) x (dims 0-7 | 8-15) of each 16-dim tile, transposed on the way
+                const uint32_t va = smem_u32(vb);
+                const int key = (lane & 7) + 8 * (lane >> 4), unit = (lane >> 3) & 1;
+                uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;  // keys 2c, 2c+1 and 2c+8, 2c+9 of a register
+                if (partial) {
+                    const auto pair = [&](int k) {
+                        return (vis.sees(pos0 + k) ? 0xFFFFu : 0u) | (vis.sees(pos0 + k + 1) ? 0xFFFF0000u : 0u);
+                    };
+                    keep0 = pair(2 * c);
+                    keep1 = pair(2 * c + 8);
+                }
+#pragma unroll
+                for (int mt = 0; mt < DV / 16; ++mt) {
+                    uint32_t v0, v1, v2, v3;
+                    ldsm_x4_t(va + v_place<false>(key, 2 * mt + unit), v0, v1, v2, v3);
+                    if (partial) v0 &= keep0, v1 &= keep0, v2 &= keep1, v3 &= keep1;
+                    mma_bf16(o[mt], v0, v1, v2, v3, ph0, ph1);
+                    mma_bf16(o[mt], v0, v1, v2, v3, pl0, pl1);
                 }
             }
         }
@@ -447,14 +480,25 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
         l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
     if (g8 == 0) *reinterpret_cast<float4 *>(ml + (warp * 8 + 2 * c) * 2) = make_float4(m0, l0, m1, l1);
+    if constexpr (E4M3) {
+#pragma unroll
+        for (int mt = 0; mt < DV / 16; ++mt) o[mt][0] *= vs_unit, o[mt][1] *= vs_unit, o[mt][2] *= vs_unit, o[mt][3] *= vs_unit;
+    }
     __syncthreads();
+    // rows g8 and g8 + 8 of tile mt: dims 16 g8 + 2 mt, + 1 (e4m3) or 16 mt + g8, + 8 (bf16)
+    const auto put = [&](int h, int mt, float x, float y) {
+        float *dst = red + (warp * HEADS + h) * DV;
+        if constexpr (E4M3) {
+            *reinterpret_cast<float2 *>(dst + 16 * g8 + 2 * mt) = make_float2(x, y);
+        } else {
+            dst[16 * mt + g8] = x;
+            dst[16 * mt + g8 + 8] = y;
+        }
+    };
 #pragma unroll
     for (int mt = 0; mt < DV / 16; ++mt) {
-        const int d = 16 * g8 + 2 * mt;
-        if (2 * c < HEADS)
-            *reinterpret_cast<float2 *>(red + (warp * HEADS + 2 * c) * DV + d) = make_float2(o[mt][0], o[mt][2]);
-        if (2 * c + 1 < HEADS)
-            *reinterpret_cast<float2 *>(red + (warp * HEADS + 2 * c + 1) * DV + d) = make_float2(o[mt][1], o[mt][3]);
+        if (2 * c < HEADS) put(2 * c, mt, o[mt][0], o[mt][2]);
+        if (2 * c + 1 < HEADS) put(2 * c + 1, mt, o[mt][1], o[mt][3]);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < HEADS * DV; i += C::THREADS) {
