@@ -673,6 +673,8 @@ gdla_status_t gdla_attn_decode_latent(const void *q_abs_sig, const void *q_abs_n
     return GDLA_OK;
 }
 
+static int shift_of(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
+
 // What both paged-cache calls check of the cache itself.
 static gdla_status_t check_cache(const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale,
                                  int cache_type, int num_pages, int page_size, const int32_t *block_table,
@@ -708,7 +710,7 @@ gdla_status_t gdla_cache_append(const void *k_nope, long long k_nope_token_strid
     if (num_new_tokens < 0 || !aligned4(cu_seqlens_new)) return GDLA_ERR_INVALID_ARG;
     if (num_new_tokens == 0) return GDLA_OK;
     if (!aligned16(k_nope) || !aligned16(k_rope) || !aligned16(v)) return GDLA_ERR_INVALID_ARG;
-    if (num_new_tokens / page_size + 2ll * batch >= (1ll << 31)) return GDLA_ERR_INVALID_ARG;
+    if ((num_new_tokens / page_size + 2ll * batch) * num_kv_heads >= (1ll << 31)) return GDLA_ERR_INVALID_ARG;
     AppendPlan p{};
     p.k_nope = static_cast<const __nv_bfloat16 *>(k_nope);
     p.k_rope = static_cast<const __nv_bfloat16 *>(k_rope);
@@ -728,6 +730,7 @@ gdla_status_t gdla_cache_append(const void *k_nope, long long k_nope_token_strid
     p.num_pages = num_pages;
     p.page_size = page_size;
     p.max_pages = max_pages_per_seq;
+    p.page_shift = shift_of(page_size);
     p.num_tokens = num_new_tokens;
     p.batch = batch;
     p.hkv = num_kv_heads;
@@ -768,7 +771,7 @@ gdla_status_t gdla_attn_decode_paged(const void *q_sig, const void *q_noise, con
     p.ws = static_cast<float *>(workspace);
     p.splits = split.cluster * split.parts;
     p.cluster = split.cluster;
-    p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    p.page_shift = shift_of(page_size);
     p.q_sig = static_cast<const __nv_bfloat16 *>(q_sig);
     p.q_noise = static_cast<const __nv_bfloat16 *>(q_noise);
     p.k_pages = k_pages;

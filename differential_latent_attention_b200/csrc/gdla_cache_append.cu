@@ -14,6 +14,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "gdla_internal.h"
 #include "gdla_paged.cuh"
 #include "gdla_ptx.cuh"
@@ -30,109 +32,359 @@ struct AppendUnit {
     int slot0, slot1;    // slots that the call fills
     int tok0;            // token of slot0
 };
+// The whole warp calls. The sequence is the last one whose first unit is <= u: each round the
+// lanes try 32 places of what is left, so 1,024 sequences take two dependent loads.
 __device__ __forceinline__ AppendUnit append_unit(const AppendPlan &p, int u) {
     AppendUnit a{};
-    int b = 0, hi = p.batch;  // last b whose first unit is <= u
-    while (hi - b > 1) {
-        const int mid = (b + hi) / 2;
-        if (p.cu_new[mid] / p.page_size + 2 * mid <= u)
-            b = mid;
-        else
-            hi = mid;
+    const int lane = threadIdx.x & 31;
+    int b = 0, left = p.batch;  // it is one of b .. b + left - 1
+    while (left > 1) {
+        const int step = (left + 31) / 32, mine = b + lane * step;
+        const bool before = lane * step < left && (p.cu_new[mine] >> p.page_shift) + 2 * mine <= u;
+        const int hits = __popc(__ballot_sync(0xffffffffu, before));
+        const int skip = max(hits - 1, 0) * step;
+        b += skip;
+        left = min(step, left - skip);
     }
     const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1], len = p.seqlens_k[b];
-    const int n = c1 - c0, before = len - n;
-    if (c0 < 0 || n < 1 || c1 > p.num_tokens || before < 0 || len > p.max_pages * static_cast<long long>(p.page_size))
-        return a;
-    const int P = p.page_size;
-    const int j = before / P + (u - (c0 / P + 2 * b));
-    if (u < c0 / P + 2 * b || j > (len - 1) / P) return a;
+    const int n = c1 - c0, before = len - n, P = p.page_size;
+    if (c0 < 0 || n < 1 || c1 > p.num_tokens || before < 0 || len > p.max_pages * static_cast<long long>(P)) return a;
+    const int first = (c0 >> p.page_shift) + 2 * b, j = (before >> p.page_shift) + (u - first);
+    if (u < first || j > (len - 1) >> p.page_shift) return a;
     a.page = p.block_table[static_cast<size_t>(b) * p.max_pages + j];
     a.live = a.page >= 0 && a.page < p.num_pages;
-    a.pos0 = j * P;
+    a.pos0 = j << p.page_shift;
     a.slot0 = max(before, a.pos0) - a.pos0;
-    a.slot1 = min(len, a.pos0 + P) - a.pos0;
+    a.slot1 = min(len - a.pos0, P);
     a.tok0 = c0 + a.pos0 + a.slot0 - before;
     return a;
 }
 
-__device__ __forceinline__ float block_max(float x, float *red) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Largest |x| of eight bf16 as fp32 bits: integers order like the numbers, and what is not
+// finite is 0x7F800000 or more.
+__device__ __forceinline__ uint32_t max_bits(const uint4 &x) {
+    const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+    return max(m << 16, m & 0xFFFF0000u);
+}
+constexpr uint32_t kInfBits = 0x7F800000u;
+// The same over the finite ones alone (the rare case).
+__device__ __forceinline__ uint32_t finite_max_bits(const uint4 &x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t m = 0u;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-    __syncthreads();
-    if (lane == 0) red[warp] = x;
-    __syncthreads();
-    x = red[0];
-    for (int i = 1; i < static_cast<int>(blockDim.x) / 32; ++i) x = fmaxf(x, red[i]);
-    return x;
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = (w[i] << 16) & 0x7FFFFFFFu, hi = w[i] & 0x7FFF0000u;
+        m = max(m, max(lo < kInfBits ? lo : 0u, hi < kInfBits ? hi : 0u));
+    }
+    return m;
+}
+// Eight bf16 times inv as e4m3 codes.
+__device__ __forceinline__ uint2 to_e4m3(const uint4 &x, float inv, bool all_finite) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
+        if (!all_finite) lo = finite_or_nan(lo), hi = finite_or_nan(hi);
+        r[i] = pack_e4m3x2(lo * inv, hi * inv);
+    }
+    return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+}
+__device__ __forceinline__ uint2 to_e4m3(const float (&x)[8], float inv, bool all_finite) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = pack_e4m3x2((all_finite ? x[2 * i] : finite_or_nan(x[2 * i])) * inv,
+                           (all_finite ? x[2 * i + 1] : finite_or_nan(x[2 * i + 1])) * inv);
+    return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+}
+__device__ __forceinline__ uint4 to_bf16(const float (&x)[8]) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ uint32_t max_bits(const float (&x)[8], bool finite_only) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t v = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+        m = max(m, finite_only && v >= kInfBits ? 0u : v);
+    }
+    return m;
 }
 
-// One block per (unit, KV head); every value by itself.
-template <bool E4M3>
-__global__ void __launch_bounds__(256)
-gdla_cache_append_kernel(const AppendPlan p) {
-    __shared__ float red[8];
+// Rotary dims 8 q .. 8 q + 7 and their partners 32 + 8 q .. of one token, turned.
+struct RopePart {
+    float lo[8], hi[8];
+};
+__device__ __forceinline__ RopePart rope_part(const AppendPlan &p, int token, int pos, int q) {
+    const __nv_bfloat16 *src = p.k_rope + static_cast<size_t>(token) * p.rope_token + 8 * q;
+    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src)), b = __ldg(reinterpret_cast<const uint4 *>(src + 32));
+    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+    RopePart r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        r.lo[i] = __uint_as_float((i & 1) ? aw[i >> 1] & 0xFFFF0000u : aw[i >> 1] << 16);
+        r.hi[i] = __uint_as_float((i & 1) ? bw[i >> 1] & 0xFFFF0000u : bw[i >> 1] << 16);
+    }
+    if (p.rotate) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float c, s;
+            rotary_angle(pos, 8 * q + i, c, s);
+            const float x = r.lo[i], y = r.hi[i];
+            r.lo[i] = x * c - y * s;
+            r.hi[i] = x * s + y * c;
+        }
+    }
+    return r;
+}
+
+// Codes of `bytes` bytes (a multiple of 8, 8-byte aligned) times a power of two <= 1, in place,
+// by `threads` threads of which this is `t`.
+__device__ __forceinline__ void shrink_codes(uint8_t *codes, int bytes, float by, int t, int threads) {
+    for (int i = t; i < bytes / 8; i += threads) {
+        uint2 x = reinterpret_cast<uint2 *>(codes)[i];
+        const auto two = [by](uint32_t c) {
+            const uint32_t h = e4m3x2_to_f16x2(c);
+            const __half2 v = *reinterpret_cast<const __half2 *>(&h);
+            return pack_e4m3x2(__low2float(v) * by, __high2float(v) * by);
+        };
+        x.x = two(x.x & 0xFFFFu) | (two(x.x >> 16) << 16);
+        x.y = two(x.y & 0xFFFFu) | (two(x.y >> 16) << 16);
+        reinterpret_cast<uint2 *>(codes)[i] = x;
+    }
+}
+// The block's exponent from its new tokens' largest |x|, the scale it had and whether it goes on.
+__device__ __forceinline__ int block_exponent(uint32_t amax_bits, bool goes_on, float had, float &shrink) {
+    int e = scale_exponent(__uint_as_float(amax_bits));
+    shrink = 1.f;
+    if (goes_on) {
+        const int was = exponent_of_scale(had);
+        e = max(e, was);
+        shrink = power_of_two(max(was - e, -126));
+    }
+    return e;
+}
+
+// Whole pages: one CTA per (unit, HEADS heads). A page and head's new values stay in registers
+// between the search for the largest and the writing, so each input is read once; the turned rotary
+// key is shared by the CTA's heads. NI = page_size / 16: 16-byte pieces of K's content (and of
+// V) per thread.
+template <bool E4M3, int NI>
+__global__ void __launch_bounds__(256, NI <= 4 ? 3 : 2)
+gdla_cache_append_kernel(const __grid_constant__ AppendPlan p) {
+    constexpr int NR = NI <= 4 ? 1 : NI / 4;  // rotary pieces (8 pairs) per thread
+    __shared__ uint32_t red[2][2][8];
     const AppendUnit a = append_unit(p, blockIdx.x);
     if (!a.live) return;
-    const int h = blockIdx.y, P = p.page_size, n = a.slot1 - a.slot0;
-    const size_t blk = static_cast<size_t>(a.page) * p.hkv + h;
-    const auto key = [&](int i, int d) {
-        const size_t t = static_cast<size_t>(a.tok0 + i);
-        if (d < 128) return __bfloat162float(p.k_nope[t * p.nope_token + static_cast<size_t>(h) * p.nope_head + d]);
-        const __nv_bfloat16 *r = p.k_rope + t * p.rope_token;
-        if (!p.rotate) return __bfloat162float(r[d - 128]);
-        const int pair = (d - 128) & 31;
-        float c, s;
-        rotary_angle(a.pos0 + a.slot0 + i, pair, c, s);
-        const float x0 = __bfloat162float(r[pair]), x1 = __bfloat162float(r[pair + 32]);
-        return d < 160 ? x0 * c - x1 * s : x0 * s + x1 * c;
-    };
-    const auto value = [&](int i, int d) {
-        return __bfloat162float(p.v[static_cast<size_t>(a.tok0 + i) * p.v_token + static_cast<size_t>(h) * p.v_head + d]);
-    };
-    const auto put = [&](auto get, void *pages, float *scale, int D) {
-        if constexpr (!E4M3) {
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(pages) + (blk * P + a.slot0) * D;
-            for (int i = threadIdx.x; i < n * D; i += blockDim.x) dst[i] = __float2bfloat16_rn(get(i / D, i % D));
-        } else {
-            float amax = 0.f;
-            for (int i = threadIdx.x; i < n * D; i += blockDim.x) amax = fmaxf(amax, finite_abs(get(i / D, i % D)));
-            int e = scale_exponent(block_max(amax, red));
-            uint8_t *dst = static_cast<uint8_t *>(pages) + blk * P * D;
-            if (a.slot0 > 0) {  // the page goes on: the larger scale of the two, older codes to it
-                const int was = exponent_of_scale(scale[blk]);
-                e = max(e, was);
-                const float shrink = power_of_two(max(was - e, -126));
-                if (was < e)
-                    for (int i = threadIdx.x; i < a.slot0 * D / 2; i += blockDim.x) {
-                        const uint32_t two = e4m3x2_to_f16x2(reinterpret_cast<uint16_t *>(dst)[i]);
-                        const __half2 hv = *reinterpret_cast<const __half2 *>(&two);
-                        reinterpret_cast<uint16_t *>(dst)[i] =
-                            pack_e4m3x2(__low2float(hv) * shrink, __high2float(hv) * shrink);
-                    }
-            }
-            const float inv = power_of_two(-e);
-            for (int i = threadIdx.x; i < n * D / 2; i += blockDim.x) {
-                const int t = 2 * i / D, d = 2 * i % D;
-                reinterpret_cast<uint16_t *>(dst + a.slot0 * D)[i] =
-                    pack_e4m3x2(finite_or_nan(get(t, d)) * inv, finite_or_nan(get(t, d + 1)) * inv);
-            }
-            __syncthreads();
-            if (threadIdx.x == 0) scale[blk] = power_of_two(e);
+    const int n = a.slot1 - a.slot0, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int row = t >> 4, col = t & 15;     // pieces (row + 16 i, col)
+    const int rrow = t >> 2, rq = t & 3;      // rotary pieces (rrow + 64 i, rq)
+    RopePart rope[NR];
+    uint32_t rope_max = 0u;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int r = rrow + 64 * i;
+        if (r < n) {
+            rope[i] = rope_part(p, a.tok0 + r, a.pos0 + a.slot0 + r, rq);
+            if (E4M3) rope_max = max(rope_max, max(max_bits(rope[i].lo, false), max_bits(rope[i].hi, false)));
         }
-    };
-    put(key, p.k_pages, p.k_scale, 192);
-    put(value, p.v_pages, p.v_scale, 128);
+    }
+    const int h0 = blockIdx.y * p.heads_per_cta, h1 = min(p.hkv, h0 + p.heads_per_cta);
+    for (int h = h0; h < h1; ++h) {
+        const size_t blk = static_cast<size_t>(a.page) * p.hkv + h;
+        uint4 k[NI], v[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+            const int r = row + 16 * i;
+            if (r < n) {
+                const size_t tok = static_cast<size_t>(a.tok0 + r);
+                k[i] = __ldg(reinterpret_cast<const uint4 *>(p.k_nope + tok * p.nope_token + h * p.nope_head + 8 * col));
+                v[i] = __ldg(reinterpret_cast<const uint4 *>(p.v + tok * p.v_token + h * p.v_head + 8 * col));
+            }
+        }
+        const size_t slot = (blk << p.page_shift) + a.slot0;
+        if constexpr (!E4M3) {
+            __nv_bfloat16 *kd = static_cast<__nv_bfloat16 *>(p.k_pages) + slot * 192;
+            __nv_bfloat16 *vd = static_cast<__nv_bfloat16 *>(p.v_pages) + slot * 128;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int r = row + 16 * i;
+                if (r < n) {
+                    *reinterpret_cast<uint4 *>(kd + r * 192 + 8 * col) = k[i];
+                    *reinterpret_cast<uint4 *>(vd + r * 128 + 8 * col) = v[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int r = rrow + 64 * i;
+                if (r < n) {
+                    *reinterpret_cast<uint4 *>(kd + r * 192 + 128 + 8 * rq) = to_bf16(rope[i].lo);
+                    *reinterpret_cast<uint4 *>(kd + r * 192 + 160 + 8 * rq) = to_bf16(rope[i].hi);
+                }
+            }
+        } else {
+            const bool goes_on = a.slot0 > 0;
+            const float k_had = goes_on ? p.k_scale[blk] : 0.f, v_had = goes_on ? p.v_scale[blk] : 0.f;
+            const auto over_block = [&](uint32_t km, uint32_t vm, uint32_t (&buf)[2][8]) {
+                km = __reduce_max_sync(0xffffffffu, km);
+                vm = __reduce_max_sync(0xffffffffu, vm);
+                if (lane == 0) buf[0][warp] = km, buf[1][warp] = vm;
+                __syncthreads();
+                km = __reduce_max_sync(0xffffffffu, buf[0][lane & 7]);
+                vm = __reduce_max_sync(0xffffffffu, buf[1][lane & 7]);
+                return make_uint2(km, vm);
+            };
+            uint32_t km = rope_max, vm = 0u;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) km = max(km, max_bits(k[i])), vm = max(vm, max_bits(v[i]));
+            uint2 m = over_block(km, vm, red[h & 1]);
+            const bool fine = m.x < kInfBits && m.y < kInfBits;
+            if (!fine) {  // infinities or NaN among them: once more without
+                km = vm = 0u;
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+                    if (rrow + 64 * i < n) km = max(km, max(max_bits(rope[i].lo, true), max_bits(rope[i].hi, true)));
+#pragma unroll
+                for (int i = 0; i < NI; ++i) km = max(km, finite_max_bits(k[i])), vm = max(vm, finite_max_bits(v[i]));
+                __syncthreads();
+                m = over_block(km, vm, red[h & 1]);
+            }
+            float k_shrink, v_shrink;
+            const int ke = block_exponent(m.x, goes_on, k_had, k_shrink);
+            const int ve = block_exponent(m.y, goes_on, v_had, v_shrink);
+            uint8_t *kd = static_cast<uint8_t *>(p.k_pages) + slot * 192;
+            uint8_t *vd = static_cast<uint8_t *>(p.v_pages) + slot * 128;
+            if (k_shrink < 1.f) shrink_codes(kd - a.slot0 * 192, a.slot0 * 192, k_shrink, t, 256);
+            if (v_shrink < 1.f) shrink_codes(vd - a.slot0 * 128, a.slot0 * 128, v_shrink, t, 256);
+            const float ki = power_of_two(-ke), vi = power_of_two(-ve);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int r = row + 16 * i;
+                if (r < n) {
+                    *reinterpret_cast<uint2 *>(kd + r * 192 + 8 * col) = to_e4m3(k[i], ki, fine);
+                    *reinterpret_cast<uint2 *>(vd + r * 128 + 8 * col) = to_e4m3(v[i], vi, fine);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int r = rrow + 64 * i;
+                if (r < n) {
+                    *reinterpret_cast<uint2 *>(kd + r * 192 + 128 + 8 * rq) = to_e4m3(rope[i].lo, ki, fine);
+                    *reinterpret_cast<uint2 *>(kd + r * 192 + 160 + 8 * rq) = to_e4m3(rope[i].hi, ki, fine);
+                }
+            }
+            // every thread has read the old scales (before the reduction's barrier)
+            if (t == 0) p.k_scale[blk] = power_of_two(ke), p.v_scale[blk] = power_of_two(ve);
+        }
+    }
 }
 
-cudaError_t launch_cache_append(const AppendPlan &p, bool e4m3, cudaStream_t stream) {
+// Few tokens per sequence (a decode step): one warp per (unit, head), row by row; lanes 0..15 hold
+// a row's K content, 16..31 its V, and lanes 0..3 the rotary part as well.
+template <bool E4M3>
+__global__ void __launch_bounds__(128)
+gdla_cache_append_step_kernel(const __grid_constant__ AppendPlan p, int units) {
+    const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int u = w / p.hkv, h = w - u * p.hkv;
+    if (u >= units) return;
+    const AppendUnit a = append_unit(p, u);
+    if (!a.live) return;
+    const int n = a.slot1 - a.slot0;
+    const bool is_k = lane < 16;
+    const __nv_bfloat16 *src = is_k ? p.k_nope + static_cast<size_t>(a.tok0) * p.nope_token + h * p.nope_head + 8 * lane
+                                    : p.v + static_cast<size_t>(a.tok0) * p.v_token + h * p.v_head + 8 * (lane - 16);
+    const long long step = is_k ? p.nope_token : p.v_token;
+    const auto piece = [&](int r) { return __ldg(reinterpret_cast<const uint4 *>(src + r * step)); };
+    const auto turned = [&](int r) { return rope_part(p, a.tok0 + r, a.pos0 + a.slot0 + r, lane & 3); };
+    const size_t blk = static_cast<size_t>(a.page) * p.hkv + h, slot = (blk << p.page_shift) + a.slot0;
+    if constexpr (!E4M3) {
+        __nv_bfloat16 *kd = static_cast<__nv_bfloat16 *>(p.k_pages) + slot * 192;
+        __nv_bfloat16 *vd = static_cast<__nv_bfloat16 *>(p.v_pages) + slot * 128;
+        for (int r = 0; r < n; ++r) {
+            const uint4 x = piece(r);
+            *reinterpret_cast<uint4 *>(is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16)) = x;
+            if (lane < 4) {
+                const RopePart q = turned(r);
+                *reinterpret_cast<uint4 *>(kd + r * 192 + 128 + 8 * lane) = to_bf16(q.lo);
+                *reinterpret_cast<uint4 *>(kd + r * 192 + 160 + 8 * lane) = to_bf16(q.hi);
+            }
+        }
+    } else {
+        const bool goes_on = a.slot0 > 0;
+        const float k_had = goes_on ? p.k_scale[blk] : 0.f, v_had = goes_on ? p.v_scale[blk] : 0.f;
+        uint32_t km = 0u, vm = 0u;
+        bool fine = true;
+        uint4 x0 = make_uint4(0u, 0u, 0u, 0u);
+        RopePart q0;
+        for (int r = 0; r < n; ++r) {  // the last row stays for the writing: with one row nothing is read twice
+            x0 = piece(r);
+            const uint32_t raw = max_bits(x0);
+            fine &= raw < kInfBits;
+            uint32_t m = raw < kInfBits ? raw : finite_max_bits(x0);
+            if (is_k) km = max(km, m); else vm = max(vm, m);
+            if (lane < 4) {
+                q0 = turned(r);
+                const uint32_t rr = max(max_bits(q0.lo, false), max_bits(q0.hi, false));
+                fine &= rr < kInfBits;
+                km = max(km, max(max_bits(q0.lo, true), max_bits(q0.hi, true)));
+            }
+        }
+        km = __reduce_max_sync(0xffffffffu, km);
+        vm = __reduce_max_sync(0xffffffffu, vm);
+        float k_shrink, v_shrink;
+        const int ke = block_exponent(km, goes_on, k_had, k_shrink);
+        const int ve = block_exponent(vm, goes_on, v_had, v_shrink);
+        uint8_t *kd = static_cast<uint8_t *>(p.k_pages) + slot * 192;
+        uint8_t *vd = static_cast<uint8_t *>(p.v_pages) + slot * 128;
+        if (k_shrink < 1.f) shrink_codes(kd - a.slot0 * 192, a.slot0 * 192, k_shrink, lane, 32);
+        if (v_shrink < 1.f) shrink_codes(vd - a.slot0 * 128, a.slot0 * 128, v_shrink, lane, 32);
+        const float ki = power_of_two(-ke), vi = power_of_two(-ve);
+        for (int r = n - 1; r >= 0; --r) {
+            if (r < n - 1) {
+                x0 = piece(r);
+                if (lane < 4) q0 = turned(r);
+            }
+            *reinterpret_cast<uint2 *>(is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16)) =
+                to_e4m3(x0, is_k ? ki : vi, fine);
+            if (lane < 4) {
+                *reinterpret_cast<uint2 *>(kd + r * 192 + 128 + 8 * lane) = to_e4m3(q0.lo, ki, fine);
+                *reinterpret_cast<uint2 *>(kd + r * 192 + 160 + 8 * lane) = to_e4m3(q0.hi, ki, fine);
+            }
+        }
+        if (lane == 0 && (k_had != power_of_two(ke) || v_had != power_of_two(ve)))
+            p.k_scale[blk] = power_of_two(ke), p.v_scale[blk] = power_of_two(ve);
+    }
+}
+
+template <bool E4M3>
+static void launch_append_pages(const AppendPlan &p, dim3 grid, cudaStream_t stream) {
+    switch (p.page_size) {
+        case 16: gdla_cache_append_kernel<E4M3, 1><<<grid, 256, 0, stream>>>(p); break;
+        case 32: gdla_cache_append_kernel<E4M3, 2><<<grid, 256, 0, stream>>>(p); break;
+        case 64: gdla_cache_append_kernel<E4M3, 4><<<grid, 256, 0, stream>>>(p); break;
+        default: gdla_cache_append_kernel<E4M3, 8><<<grid, 256, 0, stream>>>(p); break;
+    }
+}
+
+cudaError_t launch_cache_append(const AppendPlan &plan, bool e4m3, cudaStream_t stream) {
+    AppendPlan p = plan;
     const long long units = p.num_tokens / p.page_size + 2ll * p.batch;
-    const dim3 grid(static_cast<unsigned>(units), p.hkv);
+    if (p.num_tokens <= 2ll * p.batch) {
+        const unsigned grid = static_cast<unsigned>((units * p.hkv + 3) / 4);
+        if (e4m3)
+            gdla_cache_append_step_kernel<true><<<grid, 128, 0, stream>>>(p, static_cast<int>(units));
+        else
+            gdla_cache_append_step_kernel<false><<<grid, 128, 0, stream>>>(p, static_cast<int>(units));
+        return cudaPeekAtLastError();
+    }
+    // heads of a CTA: as many as share the rotary part while the card still gets several CTAs per SM
+    p.heads_per_cta = static_cast<int>(std::min<long long>(4, std::max<long long>(1, units * p.hkv / (8 * kPlanSms))));
+    const dim3 grid(static_cast<unsigned>(units), (p.hkv + p.heads_per_cta - 1) / p.heads_per_cta);
     if (e4m3)
-        gdla_cache_append_kernel<true><<<grid, 256, 0, stream>>>(p);
+        launch_append_pages<true>(p, grid, stream);
     else
-        gdla_cache_append_kernel<false><<<grid, 256, 0, stream>>>(p);
+        launch_append_pages<false>(p, grid, stream);
     return cudaPeekAtLastError();
 }
 

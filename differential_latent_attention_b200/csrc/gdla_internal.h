@@ -221,6 +221,8 @@ LatentPlan make_latent_plan(int batch, int hkv, int max_seqlen_k, int window, in
 size_t latent_workspace_bytes(const LatentPlan &plan);
 cudaError_t launch_decode_latent(const LatentLaunch &launch, const LatentPlan &plan, cudaStream_t stream);
 
+constexpr int kPlanSms = 148;  // SMs that the paged kernels' plans count on
+
 // Paged KV cache: k_pages [num_pages, H, P, 192] and v_pages [num_pages, H, P, 128] in bf16,
 // or in e4m3 with scales [num_pages, H]; block_table [batch, max_pages] names each
 // sequence's pages in order. All pointers are device memory, strides in elements.
@@ -230,7 +232,8 @@ struct AppendPlan {
     void *k_pages, *v_pages;
     float *k_scale, *v_scale;
     const int32_t *block_table, *cu_new, *seqlens_k;
-    int num_pages, page_size, max_pages, num_tokens, batch, hkv;
+    int num_pages, page_size, page_shift, max_pages, num_tokens, batch, hkv;
+    int heads_per_cta;  // set by the launch
     bool rotate;
 };
 cudaError_t launch_cache_append(const AppendPlan &plan, bool e4m3, cudaStream_t stream);
@@ -251,7 +254,6 @@ struct PagedDecode {
 struct PagedSplit {
     int cluster, parts;  // CTAs per cluster, clusters per (sequence, KV head)
 };
-constexpr int kPlanSms = 148;  // SMs that the split plan counts on
 PagedSplit paged_split(int batch, int hkv, int max_seqlen_k, int window, int sinks);
 size_t paged_workspace_bytes(int batch, int hkv, const PagedSplit &split);
 cudaError_t launch_decode_paged(const PagedDecode &plan, bool e4m3, cudaStream_t stream);

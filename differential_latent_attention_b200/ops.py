@@ -32,6 +32,7 @@ LATENT_MAX_KV_HEADS = 16
 MAX_SINKS = 128
 PAGE_SIZES = (16, 32, 64, 128)
 CACHE_BF16, CACHE_E4M3 = 0, 1
+ERR_WORKSPACE = 3
 SELFTEST_SITE = 0x30001  # GDLA_SELFTEST_SITE
 
 _lib = None
@@ -111,7 +112,7 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())  # current_stream(), without its object
     return stream.cuda_stream
 
 
@@ -131,6 +132,15 @@ def _on_one_device(stream, named):
     sdev = stream.device.index if stream is not None else torch.cuda.current_device()
     if dev is not None and sdev != dev:
         raise ValueError(f"the tensors are on cuda:{dev} but the launch stream is on cuda:{sdev}")
+
+
+def _scratch(nbytes, device, stream):
+    """Workspace of a call that was given none. The allocator may hand the memory on as soon as the call returns, so a
+    launch stream other than the current one is made known to it."""
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
 
 
 def _check_workspace(ws):
@@ -230,7 +240,7 @@ def attn_bwd(q_sig, q_noise, k, v, lam, gate, dout, seqlens, window=0, grads=Non
         _check(grads[name], name, dt, shape)
     need = attn_bwd_sinks_workspace_bytes(lens, hkv, window, sinks) if sinks else attn_bwd_workspace_bytes(n, hkv)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q_sig.device)
+        workspace = _scratch(need, q_sig.device, stream)
     _check_workspace(workspace)
     _on_one_device(stream, [("q_sig", q_sig), ("q_noise", q_noise), ("k", k), ("v", v), ("lam", lam),
                             ("gate", gate), ("dout", dout), ("workspace", workspace)] + list(grads.items()))
@@ -282,7 +292,7 @@ def prologue(x, w_qa, w_kva, gamma_q, gamma_kv, w_qb, w_uk, w_uv, w_lambda, w_ga
     for name, (shape, dt) in shapes.items():
         _check(outs[name], name, dt, shape)
     if workspace is None:
-        workspace = torch.empty(max(prologue_workspace_bytes(n), 1), dtype=torch.uint8, device=x.device)
+        workspace = _scratch(prologue_workspace_bytes(n), x.device, stream)
     _check_workspace(workspace)
     _on_one_device(stream, [("x", x), ("w_qa", w_qa), ("w_kva", w_kva), ("gamma_q", gamma_q), ("gamma_kv", gamma_kv),
                             ("w_qb", w_qb), ("w_uk", w_uk), ("w_uv", w_uv), ("w_lambda", w_lambda),
@@ -327,7 +337,7 @@ def attn_decode(q_sig, q_noise, k_cache, v_cache, cu_seqlens_k, max_seqlen_k, la
     _check(out, "out", torch.bfloat16, (b, hs, DV))
     need = decode_workspace_bytes(b, hkv, max_seqlen_k, window)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_sig.device)
+        workspace = _scratch(need, q_sig.device, stream)
     _check_workspace(workspace)
     _on_one_device(stream, (("q_sig", q_sig), ("q_noise", q_noise), ("k_cache", k_cache), ("v_cache", v_cache),
                             ("cu_seqlens_k", cu_seqlens_k), ("lam", lam), ("gate", gate), ("out", out),
@@ -372,7 +382,7 @@ def attn_decode_latent(q_abs_sig, q_abs_noise, ckv, cu_seqlens_k, max_seqlen_k, 
     _check(out, "out", torch.bfloat16, (b, hs, DV))
     need = decode_latent_workspace_bytes(b, hkv, max_seqlen_k, window)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_abs_sig.device)
+        workspace = _scratch(need, q_abs_sig.device, stream)
     _check_workspace(workspace)
     _on_one_device(stream, (("q_abs_sig", q_abs_sig), ("q_abs_noise", q_abs_noise), ("ckv", ckv),
                             ("cu_seqlens_k", cu_seqlens_k), ("w_uv", w_uv), ("lam", lam), ("gate", gate),
@@ -387,8 +397,25 @@ def attn_decode_latent(q_abs_sig, q_abs_noise, ckv, cu_seqlens_k, max_seqlen_k, 
     return out
 
 
-def _check_cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k):
-    """The paged cache's own arguments: (cache type, pages, KV heads, page size, batch, table width)."""
+# The paged-cache calls are made once per layer and token, so their checks are one
+# combined test per tensor, which hands back the pointer; what failed is worked out only then.
+def _launch_device(stream):
+    return torch.cuda.current_device() if stream is None else stream.device.index
+
+
+def _dense(t, name, dtype, shape, dev):
+    """The pointer of a contiguous tensor of this type and shape on CUDA device ``dev``."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _check(t, name, dtype, shape)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's launch stream on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev):
+    """The paged cache's own arguments, checked: (sizes, pointers)."""
     if not isinstance(k_pages, torch.Tensor) or not isinstance(block_table, torch.Tensor):
         raise TypeError("k_pages and block_table must be torch.Tensors")
     if k_pages.dim() != 4 or block_table.dim() != 2:
@@ -396,40 +423,46 @@ def _check_cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k):
     np_, hkv, ps, _ = k_pages.shape
     b, width = block_table.shape
     dt = k_pages.dtype
+    ks = vs = 0
     if dt is torch.bfloat16:
         kind = CACHE_BF16
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale and v_scale belong to an e4m3 cache")
     elif dt is torch.float8_e4m3fn:
         kind = CACHE_E4M3
-        _check(k_scale, "k_scale", torch.float32, (np_, hkv))
-        _check(v_scale, "v_scale", torch.float32, (np_, hkv))
+        ks = _dense(k_scale, "k_scale", torch.float32, (np_, hkv), dev)
+        vs = _dense(v_scale, "v_scale", torch.float32, (np_, hkv), dev)
     else:
         raise TypeError(f"k_pages: expected torch.bfloat16 or torch.float8_e4m3fn, got {dt}")
-    _check(k_pages, "k_pages", dt, (np_, hkv, ps, DQK))
-    _check(v_pages, "v_pages", dt, (np_, hkv, ps, DV))
-    _check(block_table, "block_table", torch.int32, (b, width))
-    _check(seqlens_k, "seqlens_k", torch.int32, (b,))
-    return kind, np_, hkv, ps, b, width
+    kp = _dense(k_pages, "k_pages", dt, (np_, hkv, ps, DQK), dev)
+    vp = _dense(v_pages, "v_pages", dt, (np_, hkv, ps, DV), dev)
+    bt = _dense(block_table, "block_table", torch.int32, (b, width), dev)
+    sl = _dense(seqlens_k, "seqlens_k", torch.int32, (b,), dev)
+    return kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl
 
 
-def _row_strides(t, name, shape):
-    """Element strides of a bf16 CUDA tensor whose last dimension is dense (others may be views)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
+def _rows(t, name, shape, dev):
+    """(pointer, strides of all but the last dimension) of a bf16 CUDA tensor whose last dimension is dense; the
+    others may be views."""
+    if not (type(t) is torch.Tensor and t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on a CUDA device")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's launch stream on cuda:{dev}")
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}: its last dimension must be contiguous")
-    st = [0 if size == 1 else x for size, x in zip(shape, st[:-1])]   # one row: its stride says nothing
-    if any(x & 7 for x in st):
+    if shape[0] == 1 or shape[-2] == 1:
+        st = [0 if size == 1 else x for size, x in zip(shape, st)]   # one row: its stride says nothing
+    if (st[0] | st[-2]) & 7:
         raise ValueError(f"{name}: strides must be multiples of 8 elements, got {t.stride()}")
-    return st
+    return t.data_ptr(), st[0], st[-2]
 
 
 def cache_append(k_nope, k_rope, v, k_pages, v_pages, block_table, cu_seqlens_new, seqlens_k, k_scale=None,
@@ -446,19 +479,16 @@ def cache_append(k_nope, k_rope, v, k_pages, v_pages, block_table, cu_seqlens_ne
     b, which then holds seqlens_k[b] tokens. ``rotate`` turns k_rope to each token's
     position on the way. Pages and scales are updated in place.
     """
-    kind, np_, hkv, ps, b, width = _check_cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k)
+    dev = _launch_device(stream)
+    kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl = _cache(k_pages, v_pages, k_scale, v_scale, block_table,
+                                                                  seqlens_k, dev)
     n = v.shape[0]
-    kn = _row_strides(k_nope, "k_nope", (n, hkv, DQK - DR))
-    kr = _row_strides(k_rope, "k_rope", (n, DR))
-    vs = _row_strides(v, "v", (n, hkv, DV))
-    _check(cu_seqlens_new, "cu_seqlens_new", torch.int32, (b + 1,))
-    _on_one_device(stream, (("k_nope", k_nope), ("k_rope", k_rope), ("v", v), ("k_pages", k_pages),
-                            ("v_pages", v_pages), ("block_table", block_table), ("cu_seqlens_new", cu_seqlens_new),
-                            ("seqlens_k", seqlens_k), ("k_scale", k_scale), ("v_scale", v_scale)))
-    st = library().gdla_cache_append(_ptr(k_nope), kn[0], kn[1], _ptr(k_rope), kr[0], _ptr(v), vs[0], vs[1],
-                                     _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), kind, np_, ps,
-                                     _ptr(block_table), width, _ptr(cu_seqlens_new), n, _ptr(seqlens_k), b, hkv,
-                                     1 if rotate else 0, _stream(stream))
+    kn, kn_t, kn_h = _rows(k_nope, "k_nope", (n, hkv, DQK - DR), dev)
+    kr, kr_t, _ = _rows(k_rope, "k_rope", (n, DR), dev)
+    vv, v_t, v_h = _rows(v, "v", (n, hkv, DV), dev)
+    cu = _dense(cu_seqlens_new, "cu_seqlens_new", torch.int32, (b + 1,), dev)
+    st = library().gdla_cache_append(kn, kn_t, kn_h, kr, kr_t, vv, v_t, v_h, kp, vp, ks, vs, kind, np_, ps, bt, width,
+                                     cu, n, sl, b, hkv, 1 if rotate else 0, _stream(stream))
     if st != 0:
         raise GDLAError(st, "gdla_cache_append")
 
@@ -479,27 +509,31 @@ def attn_decode_paged(q_sig, q_noise, k_pages, v_pages, block_table, seqlens_k, 
     position first. ``workspace`` (uint8 CUDA tensor) is allocated here when not given.
     Returns out [B, 4H, 128] bf16.
     """
-    kind, np_, hkv, ps, b, width = _check_cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k)
+    dev = _launch_device(stream)
+    kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl = _cache(k_pages, v_pages, k_scale, v_scale, block_table,
+                                                                  seqlens_k, dev)
     hs = GROUP * hkv
-    _check(q_sig, "q_sig", torch.bfloat16, (b, hs, DQK))
-    _check(q_noise, "q_noise", torch.bfloat16, (b, hkv, DQK))
-    _check(lam, "lam", torch.float32, (b, hs))
-    _check(gate, "gate", torch.bfloat16, (b, hs, DV))
+    qs = _dense(q_sig, "q_sig", torch.bfloat16, (b, hs, DQK), dev)
+    qn = _dense(q_noise, "q_noise", torch.bfloat16, (b, hkv, DQK), dev)
+    lm = _dense(lam, "lam", torch.float32, (b, hs), dev)
+    gt = _dense(gate, "gate", torch.bfloat16, (b, hs, DV), dev)
     if out is None:
-        out = torch.empty((b, hs, DV), dtype=torch.bfloat16, device=q_sig.device)
-    _check(out, "out", torch.bfloat16, (b, hs, DV))
-    need = decode_paged_workspace_bytes(b, hkv, max_seqlen_k, window, sinks)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_sig.device)
-    _check_workspace(workspace)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _on_one_device(stream, (("q_sig", q_sig), ("q_noise", q_noise), ("k_pages", k_pages), ("v_pages", v_pages),
-                            ("block_table", block_table), ("seqlens_k", seqlens_k), ("lam", lam), ("gate", gate),
-                            ("out", out), ("workspace", workspace), ("k_scale", k_scale), ("v_scale", v_scale)))
-    st = library().gdla_attn_decode_paged(_ptr(q_sig), _ptr(q_noise), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
-                                          _ptr(v_scale), kind, np_, ps, _ptr(block_table), width, _ptr(seqlens_k),
-                                          int(max_seqlen_k), _ptr(lam), _ptr(gate), _ptr(out), b, hkv, int(window),
-                                          int(sinks), 1 if rotate else 0, _ptr(workspace), ws_bytes, _stream(stream))
+        out = torch.empty_like(gate)
+    ot = _dense(out, "out", torch.bfloat16, (b, hs, DV), dev)
+    fn = library().gdla_attn_decode_paged
+    args = (qs, qn, kp, vp, ks, vs, kind, np_, ps, bt, width, sl, int(max_seqlen_k), lm, gt, ot, b, hkv, int(window),
+            int(sinks), 1 if rotate else 0)
+    if workspace is None:
+        st = fn(*args, 0, 0, _stream(stream))
+        if st == ERR_WORKSPACE:  # the few sizes that need one
+            workspace = _scratch(decode_paged_workspace_bytes(b, hkv, max_seqlen_k, window, sinks), q_sig.device,
+                                 stream)
+            st = fn(*args, workspace.data_ptr(), workspace.numel(), _stream(stream))
+    else:
+        _check_workspace(workspace)
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace is on cuda:{workspace.get_device()}, the call's launch stream on cuda:{dev}")
+        st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
     if st != 0:
         raise GDLAError(st, "gdla_attn_decode_paged")
     return out
