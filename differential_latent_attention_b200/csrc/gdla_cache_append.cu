@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gdla_internal.h"
 #include "gdla_paged.cuh"
@@ -78,25 +79,22 @@ __device__ __forceinline__ uint32_t finite_max_bits(const uint4 &x) {
     }
     return m;
 }
-// Eight bf16 times inv as e4m3 codes.
-__device__ __forceinline__ uint2 to_e4m3(const uint4 &x, float inv, bool all_finite) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
-        if (!all_finite) lo = finite_or_nan(lo), hi = finite_or_nan(hi);
-        r[i] = pack_e4m3x2(lo * inv, hi * inv);
-    }
-    return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+// Eight values times inv as e4m3 codes; FINITE: there is no infinity or NaN among them.
+template <bool FINITE>
+__device__ __forceinline__ uint32_t pair_e4m3(float lo, float hi, float inv) {
+    return FINITE ? pack_e4m3x2(lo * inv, hi * inv) : pack_e4m3x2(finite_or_nan(lo) * inv, finite_or_nan(hi) * inv);
 }
-__device__ __forceinline__ uint2 to_e4m3(const float (&x)[8], float inv, bool all_finite) {
-    uint32_t r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        r[i] = pack_e4m3x2((all_finite ? x[2 * i] : finite_or_nan(x[2 * i])) * inv,
-                           (all_finite ? x[2 * i + 1] : finite_or_nan(x[2 * i + 1])) * inv);
-    return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+template <bool FINITE>
+__device__ __forceinline__ uint2 to_e4m3(const uint4 &x, float inv) {
+    const auto two = [inv](uint32_t w) {
+        return pair_e4m3<FINITE>(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u), inv);
+    };
+    return make_uint2(__byte_perm(two(x.x), two(x.y), 0x5410), __byte_perm(two(x.z), two(x.w), 0x5410));
+}
+template <bool FINITE>
+__device__ __forceinline__ uint2 to_e4m3(const float (&x)[8], float inv) {
+    const auto two = [&](int i) { return pair_e4m3<FINITE>(x[i], x[i + 1], inv); };
+    return make_uint2(__byte_perm(two(0), two(2), 0x5410), __byte_perm(two(4), two(6), 0x5410));
 }
 __device__ __forceinline__ uint4 to_bf16(const float (&x)[8]) {
     return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
@@ -174,7 +172,9 @@ __global__ void __launch_bounds__(256, NI <= 4 ? 3 : 2)
 gdla_cache_append_kernel(const __grid_constant__ AppendPlan p) {
     constexpr int NR = NI <= 4 ? 1 : NI / 4;  // rotary pieces (8 pairs) per thread
     __shared__ uint32_t red[2][2][8];
-    const AppendUnit a = append_unit(p, blockIdx.x);
+    const int groups = (p.hkv + p.heads_per_cta - 1) / p.heads_per_cta;
+    const int u = blockIdx.x / groups;
+    const AppendUnit a = append_unit(p, u);
     if (!a.live) return;
     const int n = a.slot1 - a.slot0, t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int row = t >> 4, col = t & 15;     // pieces (row + 16 i, col)
@@ -189,18 +189,19 @@ gdla_cache_append_kernel(const __grid_constant__ AppendPlan p) {
             if (E4M3) rope_max = max(rope_max, max(max_bits(rope[i].lo, false), max_bits(rope[i].hi, false)));
         }
     }
-    const int h0 = blockIdx.y * p.heads_per_cta, h1 = min(p.hkv, h0 + p.heads_per_cta);
-    for (int h = h0; h < h1; ++h) {
+    const int h0 = (blockIdx.x - u * groups) * p.heads_per_cta, h1 = min(p.hkv, h0 + p.heads_per_cta);
+    const size_t tok = static_cast<size_t>(a.tok0 + row);
+    const __nv_bfloat16 *k_src = p.k_nope + tok * p.nope_token + h0 * p.nope_head + 8 * col;
+    const __nv_bfloat16 *v_src = p.v + tok * p.v_token + h0 * p.v_head + 8 * col;
+    for (int h = h0; h < h1; ++h, k_src += p.nope_head, v_src += p.v_head) {
         const size_t blk = static_cast<size_t>(a.page) * p.hkv + h;
         uint4 k[NI], v[NI];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
-            const int r = row + 16 * i;
-            if (r < n) {
-                const size_t tok = static_cast<size_t>(a.tok0 + r);
-                k[i] = __ldg(reinterpret_cast<const uint4 *>(p.k_nope + tok * p.nope_token + h * p.nope_head + 8 * col));
-                v[i] = __ldg(reinterpret_cast<const uint4 *>(p.v + tok * p.v_token + h * p.v_head + 8 * col));
+            if (row + 16 * i < n) {
+                k[i] = __ldg(reinterpret_cast<const uint4 *>(k_src + 16 * i * p.nope_token));
+                v[i] = __ldg(reinterpret_cast<const uint4 *>(v_src + 16 * i * p.v_token));
             }
         }
         const size_t slot = (blk << p.page_shift) + a.slot0;
@@ -258,22 +259,29 @@ gdla_cache_append_kernel(const __grid_constant__ AppendPlan p) {
             if (k_shrink < 1.f) shrink_codes(kd - a.slot0 * 192, a.slot0 * 192, k_shrink, t, 256);
             if (v_shrink < 1.f) shrink_codes(vd - a.slot0 * 128, a.slot0 * 128, v_shrink, t, 256);
             const float ki = power_of_two(-ke), vi = power_of_two(-ve);
+            const auto write = [&](auto finite) {
+                constexpr bool FINITE = decltype(finite)::value;
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int r = row + 16 * i;
-                if (r < n) {
-                    *reinterpret_cast<uint2 *>(kd + r * 192 + 8 * col) = to_e4m3(k[i], ki, fine);
-                    *reinterpret_cast<uint2 *>(vd + r * 128 + 8 * col) = to_e4m3(v[i], vi, fine);
+                for (int i = 0; i < NI; ++i) {
+                    const int r = row + 16 * i;
+                    if (r < n) {
+                        *reinterpret_cast<uint2 *>(kd + r * 192 + 8 * col) = to_e4m3<FINITE>(k[i], ki);
+                        *reinterpret_cast<uint2 *>(vd + r * 128 + 8 * col) = to_e4m3<FINITE>(v[i], vi);
+                    }
                 }
-            }
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                const int r = rrow + 64 * i;
-                if (r < n) {
-                    *reinterpret_cast<uint2 *>(kd + r * 192 + 128 + 8 * rq) = to_e4m3(rope[i].lo, ki, fine);
-                    *reinterpret_cast<uint2 *>(kd + r * 192 + 160 + 8 * rq) = to_e4m3(rope[i].hi, ki, fine);
+                for (int i = 0; i < NR; ++i) {
+                    const int r = rrow + 64 * i;
+                    if (r < n) {
+                        *reinterpret_cast<uint2 *>(kd + r * 192 + 128 + 8 * rq) = to_e4m3<FINITE>(rope[i].lo, ki);
+                        *reinterpret_cast<uint2 *>(kd + r * 192 + 160 + 8 * rq) = to_e4m3<FINITE>(rope[i].hi, ki);
+                    }
                 }
-            }
+            };
+            if (fine)
+                write(std::true_type());
+            else
+                write(std::false_type());
             // every thread has read the old scales (before the reduction's barrier)
             if (t == 0) p.k_scale[blk] = power_of_two(ke), p.v_scale[blk] = power_of_two(ve);
         }
@@ -314,19 +322,15 @@ gdla_cache_append_step_kernel(const __grid_constant__ AppendPlan p, int units) {
         const bool goes_on = a.slot0 > 0;
         const float k_had = goes_on ? p.k_scale[blk] : 0.f, v_had = goes_on ? p.v_scale[blk] : 0.f;
         uint32_t km = 0u, vm = 0u;
-        bool fine = true;
         uint4 x0 = make_uint4(0u, 0u, 0u, 0u);
         RopePart q0;
         for (int r = 0; r < n; ++r) {  // the last row stays for the writing: with one row nothing is read twice
             x0 = piece(r);
             const uint32_t raw = max_bits(x0);
-            fine &= raw < kInfBits;
-            uint32_t m = raw < kInfBits ? raw : finite_max_bits(x0);
+            const uint32_t m = raw < kInfBits ? raw : finite_max_bits(x0);
             if (is_k) km = max(km, m); else vm = max(vm, m);
             if (lane < 4) {
                 q0 = turned(r);
-                const uint32_t rr = max(max_bits(q0.lo, false), max_bits(q0.hi, false));
-                fine &= rr < kInfBits;
                 km = max(km, max(max_bits(q0.lo, true), max_bits(q0.hi, true)));
             }
         }
@@ -345,11 +349,11 @@ gdla_cache_append_step_kernel(const __grid_constant__ AppendPlan p, int units) {
                 x0 = piece(r);
                 if (lane < 4) q0 = turned(r);
             }
-            *reinterpret_cast<uint2 *>(is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16)) =
-                to_e4m3(x0, is_k ? ki : vi, fine);
+            uint8_t *dst = is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16);
+            *reinterpret_cast<uint2 *>(dst) = to_e4m3<false>(x0, is_k ? ki : vi);
             if (lane < 4) {
-                *reinterpret_cast<uint2 *>(kd + r * 192 + 128 + 8 * lane) = to_e4m3(q0.lo, ki, fine);
-                *reinterpret_cast<uint2 *>(kd + r * 192 + 160 + 8 * lane) = to_e4m3(q0.hi, ki, fine);
+                *reinterpret_cast<uint2 *>(kd + r * 192 + 128 + 8 * lane) = to_e4m3<false>(q0.lo, ki);
+                *reinterpret_cast<uint2 *>(kd + r * 192 + 160 + 8 * lane) = to_e4m3<false>(q0.hi, ki);
             }
         }
         if (lane == 0 && (k_had != power_of_two(ke) || v_had != power_of_two(ve)))
@@ -358,7 +362,7 @@ gdla_cache_append_step_kernel(const __grid_constant__ AppendPlan p, int units) {
 }
 
 template <bool E4M3>
-static void launch_append_pages(const AppendPlan &p, dim3 grid, cudaStream_t stream) {
+static void launch_append_pages(const AppendPlan &p, unsigned grid, cudaStream_t stream) {
     switch (p.page_size) {
         case 16: gdla_cache_append_kernel<E4M3, 1><<<grid, 256, 0, stream>>>(p); break;
         case 32: gdla_cache_append_kernel<E4M3, 2><<<grid, 256, 0, stream>>>(p); break;
@@ -380,7 +384,7 @@ cudaError_t launch_cache_append(const AppendPlan &plan, bool e4m3, cudaStream_t 
     }
     // heads of a CTA: as many as share the rotary part while the card still gets several CTAs per SM
     p.heads_per_cta = static_cast<int>(std::min<long long>(4, std::max<long long>(1, units * p.hkv / (8 * kPlanSms))));
-    const dim3 grid(static_cast<unsigned>(units), (p.hkv + p.heads_per_cta - 1) / p.heads_per_cta);
+    const unsigned grid = static_cast<unsigned>(units * ((p.hkv + p.heads_per_cta - 1) / p.heads_per_cta));
     if (e4m3)
         launch_append_pages<true>(p, grid, stream);
     else
