@@ -193,8 +193,8 @@ bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int sinks
 auto q_tile_cost(int T, int key_tile, int window, int sinks) {
     return [=](int L, int qt) {
         const int t0 = qt * T;
-        const SinkTiles st = sink_tiles((window > 0) ? std::max(0, t0 - window + 1) : 0, sinks, key_tile);
-        return st.n_sink + (std::min(L, t0 + T) - st.kv_lo + key_tile - 1) / key_tile;
+        const SinkRun run = sink_run((window > 0) ? std::max(0, t0 - window + 1) : 0, sinks);
+        return (run.pre + std::min(L, t0 + T) - run.kv_lo + key_tile - 1) / key_tile;
     };
 }
 
@@ -223,6 +223,14 @@ BwdWorkspace bwd_workspace(long long n, int hkv, long long part_slots = 0, int s
     w.part = w.stats + align256(static_cast<size_t>(n) * hkv * kBwdStats * 4);
     w.total = w.part + align256(static_cast<size_t>(part_slots) * hkv * sinks * (192 + 128) * 4);
     return w;
+}
+
+// The maps of the key tile in which sinks and window meet (none where the sinks' rows end on a tile's edge).
+bool make_sink_maps(SinkMaps<true> *m, const void *k, const void *v, int hkv, uint64_t n, int sinks, int key_tile) {
+    const uint32_t first = ((sinks + 7) & ~7) % key_tile, rest = key_tile - first;
+    if (first == 0) return true;
+    return make_map(&m->k_sink, k, 192, hkv, n, 64, 1, first) && make_map(&m->k_rest, k, 192, hkv, n, 64, 1, rest) &&
+           make_map(&m->v_sink, v, 128, hkv, n, 64, 1, first) && make_map(&m->v_rest, v, 128, hkv, n, 64, 1, rest);
 }
 
 // What every prefill call checks of its lengths; *total and *longest are filled in.
@@ -334,6 +342,7 @@ static gdla_status_t attn_fwd(const void *q_sig, const void *q_noise, const void
          !make_map_f32_2d(&L.tm_lam, lambda, 4 * hkv, N, 4, kPrefillTileTokens) ||
          !make_map(&L.tm_out, out, 128, 4 * hkv, N, 64, 4, TQ)))
         return GDLA_ERR_CUDA;
+    if (sinks > 0 && !make_sink_maps(&L.sink, k, v, hkv, N, sinks, geo.key_tile)) return GDLA_ERR_CUDA;
     L.lambda = lambda;
     L.gate = static_cast<const __nv_bfloat16 *>(gate_logits);
     L.out = static_cast<__nv_bfloat16 *>(out);
@@ -408,6 +417,7 @@ static gdla_status_t attn_bwd(const void *q_sig, const void *q_noise, const void
         !make_map(&F.tm_k, k, 192, hkv, N, 64, 1, geo.key_tile) ||
         !make_map(&F.tm_v, v, 128, hkv, N, 64, 1, geo.v_box))
         return GDLA_ERR_CUDA;
+    if (sinks > 0 && !make_sink_maps(&F.sink, k, v, hkv, N, sinks, geo.key_tile)) return GDLA_ERR_CUDA;
     F.lambda = lambda;
     F.gate = static_cast<const __nv_bfloat16 *>(gate_logits);
     F.bwd = {static_cast<const __nv_bfloat16 *>(dout), static_cast<__nv_bfloat16 *>(dgate), dlambda, dh_sig, dh_noise,
@@ -433,6 +443,7 @@ static gdla_status_t attn_bwd(const void *q_sig, const void *q_noise, const void
         !make_map(&B.tm_v128, v, 128, hkv, N, 64, 1, kBwdKeyTile) ||
         !make_map_f32_3d(&B.tm_stats, stats, kBwdStats, hkv, N, kBwdStats, 1, kBwdStepTokens))
         return GDLA_ERR_CUDA;
+    if (sinks > 0 && !make_sink_maps(&B.sink64, k, v, hkv, N, sinks, kBwdQKeyTile)) return GDLA_ERR_CUDA;
     B.stats = stats;
     B.dq_sig = static_cast<__nv_bfloat16 *>(dq_sig);
     B.dq_noise = static_cast<__nv_bfloat16 *>(dq_noise);

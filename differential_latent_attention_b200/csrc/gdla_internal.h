@@ -36,17 +36,27 @@ __device__ __forceinline__ int snake_item(int r) {
     return r * g + ((r & 1) ? g - 1 - c : c);
 }
 
-// Key tiles of a q tile whose window starts at kv_lo, with `sinks` first tokens visible behind
-// it: the tiles that hold the sinks, then those from kv_lo on; where the two would meet,
-// one run from key 0. Every key is in one tile of the list.
-struct SinkTiles {
-    int n_sink, kv_lo;
+// The keys of a q tile whose window starts at kv_lo, with `sinks` first tokens visible behind it,
+// as one run of columns that the key tiles cut: `pre` columns of sinks (the count rounded up to
+// the 8 rows of a swizzle atom; the columns past it are masked), then the keys from kv_lo on.
+// With the sinks in a tile of their own a q tile of the window-128 sliding schedule would visit four
+// tiles instead of three; in the run, 48 tokens' 175 keys and up to 16 sinks are three
+// (2 x 8192 tokens, 16 heads: 335 -> 299 us). Where the two would meet, one run from key 0 (pre = 0).
+struct SinkRun {
+    int pre, kv_lo;
 };
-__host__ __device__ __forceinline__ SinkTiles sink_tiles(int kv_lo, int sinks, int key_tile) {
-    const int n = (sinks + key_tile - 1) / key_tile;
-    if (kv_lo <= n * key_tile) return {0, sinks > 0 ? 0 : kv_lo};
-    return {n, kv_lo};
+__host__ __device__ __forceinline__ SinkRun sink_run(int kv_lo, int sinks) {
+    const int pre = (sinks + 7) & ~7;
+    if (kv_lo <= pre) return {0, sinks > 0 ? 0 : kv_lo};
+    return {pre, kv_lo};
 }
+// Tensor maps of the tile in which sinks and window meet: pre % key_tile sink rows, then the rest.
+template <bool SINK>
+struct SinkMaps {};
+template <>
+struct SinkMaps<true> {
+    CUtensorMap k_sink, k_rest, v_sink, v_rest;
+};
 
 // Passed by value (kernel parameters): the q-tiles of one launch, heaviest
 // first. The host builds the largest form and launches the smallest capacity
@@ -85,6 +95,7 @@ struct BwdIO {
 
 struct PrefillLaunch {
     CUtensorMap tm_qs, tm_qn, tm_k, tm_v;
+    SinkMaps<true> sink;                  // with sinks
     CUtensorMap tm_gate, tm_lam, tm_out;  // used by the asynchronous epilogue (short windows)
     const float *lambda;
     const __nv_bfloat16 *gate;
@@ -103,6 +114,7 @@ struct BwdLaunch {
     CUtensorMap tm_dhs, tm_dhn;     // dH boxes of 6 tokens
     CUtensorMap tm_qs12, tm_qn12;   // Q boxes of 12 tokens (dkv steps)
     CUtensorMap tm_dhs12, tm_dhn12; // dH boxes of 12 tokens
+    SinkMaps<true> sink64;          // with sinks: of 64-key tiles (dq)
     CUtensorMap tm_k64, tm_v64;     // 64-key K / V boxes (dq)
     CUtensorMap tm_k128, tm_v128;   // 128-key K / V boxes (dkv)
     CUtensorMap tm_stats;           // row statistics, 12 tokens of one group

@@ -348,7 +348,8 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1)
 gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_constant__ CUtensorMap tm_qn,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_gate, const __grid_constant__ CUtensorMap tm_lam,
-                    const __grid_constant__ CUtensorMap tm_out, const float *__restrict__ lambda,
+                    const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ SinkMaps<C::SINK> sink,
+                    const float *__restrict__ lambda,
                     const __nv_bfloat16 *__restrict__ gate, __nv_bfloat16 *__restrict__ out, const BwdIO bwd,
                     const __grid_constant__ Plan plan) {
     using namespace pf;
@@ -381,17 +382,12 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
     // Item w: group = w % hkv, block = items[w / hkv]; key tiles of q tile x.
     struct Item {
         int group, s0, L, t0, kv_lo;
-        int n_sink;  // leading key tiles that hold the sinks (0 without sinks)
+        int pre;  // columns of sinks before the window's keys (0 without sinks)
         int n_tiles[TILES];
-        // first key of key tile k
-        __device__ __forceinline__ int key0(int k) const {
-            if (C::SINK) return k < n_sink ? k * C::BN : kv_lo + (k - n_sink) * C::BN;
-            return kv_lo + k * C::BN;
-        }
     };
     auto item_at = [&](int w) {
         Item it;
-        it.n_sink = 0;
+        it.pre = 0;
         it.group = w % hkv;
         const uint32_t code = plan.items[w / hkv];
         const int seq = static_cast<int>(code >> kItemSeqShift);
@@ -400,13 +396,13 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
         it.t0 = static_cast<int>(code & kItemTileMask) * C::CTA_TOK;
         it.kv_lo = (window > 0) ? max(0, it.t0 - window + 1) : 0;
         if constexpr (C::SINK) {
-            const SinkTiles st = sink_tiles(it.kv_lo, plan.sinks, BN);
-            it.n_sink = st.n_sink;
-            it.kv_lo = st.kv_lo;
+            const SinkRun run = sink_run(it.kv_lo, plan.sinks);
+            it.pre = run.pre;
+            it.kv_lo = run.kv_lo;
         }
 #pragma unroll
         for (int x = 0; x < TILES; ++x)
-            it.n_tiles[x] = it.n_sink + (min(it.L, it.t0 + (x + 1) * TOK) - it.kv_lo + BN - 1) / BN;
+            it.n_tiles[x] = (it.pre + min(it.L, it.t0 + (x + 1) * TOK) - it.kv_lo + BN - 1) / BN;
         return it;
     };
 
@@ -510,23 +506,44 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
                 for (int k = 0; ok && k < it.n_tiles[TILES - 1]; ++k, ++kv) {
                     const int st = kv % STAGES;
                     const uint32_t use = static_cast<uint32_t>(kv / STAGES);
-                    const int row = it.s0 + it.key0(k);
+                    int row = it.s0 + it.kv_lo - it.pre + k * BN;
+                    const int n_sink = C::SINK ? it.pre - k * BN : 0;  // sink rows from this tile on
+                    const bool meet = n_sink > 0 && n_sink < BN;      // sinks and window in one tile
+                    if (n_sink >= BN) row = it.s0 + k * BN;
                     if (kv >= STAGES && !mbar_wait(k_empty + st, (use + 1) & 1, abort_flag, ERR_SITE_PREFILL | 1)) {
                         ok = false;
                         break;
                     }
                     mbar_arrive_expect_tx(k_full + st, C::K_TX);
-                    for (int c = 0; c < KCHUNKS; ++c)
-                        tma_load_3d(smem + C::OFF_K + st * C::K_STAGE + c * C::KV_CHUNK, &tm_k, k_full + st, c * 64,
-                                    it.group, row);
+                    for (int c = 0; c < KCHUNKS; ++c) {
+                        uint8_t *dst = smem + C::OFF_K + st * C::K_STAGE + c * C::KV_CHUNK;
+                        if constexpr (C::SINK) {
+                            if (meet) {
+                                tma_load_3d(dst, &sink.k_sink, k_full + st, c * 64, it.group, it.s0 + k * BN);
+                                tma_load_3d(dst + n_sink * 128, &sink.k_rest, k_full + st, c * 64, it.group,
+                                            it.s0 + it.kv_lo);
+                                continue;
+                            }
+                        }
+                        tma_load_3d(dst, &tm_k, k_full + st, c * 64, it.group, row);
+                    }
                     if (kv >= STAGES && !mbar_wait(v_empty + st, (use + 1) & 1, abort_flag, ERR_SITE_PREFILL | 2)) {
                         ok = false;
                         break;
                     }
                     mbar_arrive_expect_tx(v_full + st, C::V_TX);
-                    for (int c = 0; c < VCHUNKS; ++c)
-                        tma_load_3d(smem + C::OFF_V + st * C::V_STAGE + c * C::KV_CHUNK, &tm_v, v_full + st,
-                                    c * 64, it.group, row);
+                    for (int c = 0; c < VCHUNKS; ++c) {
+                        uint8_t *dst = smem + C::OFF_V + st * C::V_STAGE + c * C::KV_CHUNK;
+                        if constexpr (C::SINK) {
+                            if (meet) {
+                                tma_load_3d(dst, &sink.v_sink, v_full + st, c * 64, it.group, it.s0 + k * BN);
+                                tma_load_3d(dst + n_sink * 128, &sink.v_rest, v_full + st, c * 64, it.group,
+                                            it.s0 + it.kv_lo);
+                                continue;
+                            }
+                        }
+                        tma_load_3d(dst, &tm_v, v_full + st, c * 64, it.group, row);
+                    }
                     issued_kv = kv + 1;
                     if (C::ASYNC_EPI && k == gate_after && !issue_gate()) {
                         ok = false;
@@ -693,14 +710,14 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
 #pragma unroll
                     for (int i = 0; i < 64; ++i) s[h * 64 + i] = __uint_as_float(rr[i]);
                 }
-                const int u0 = it.key0(k);
+                const int u0 = it.kv_lo - it.pre + k * BN;  // key of column 0 (behind the sinks' columns)
                 const bool need_mask = (u0 + BN - 1 > tx0) || (window > 0 && u0 < tx0 + TOK - window);
                 if (need_mask) {
                     // visible columns: keys lo_t..t of this row
                     const int c_lo = lo_t - u0, c_hi = t - u0;
                     if constexpr (C::SINK) {
-                        // and the sinks before the window (a sink tile lies wholly before it)
-                        const int c_sink = plan.sinks - u0;
+                        // and the sinks, whose columns come first
+                        const int c_sink = plan.sinks - k * BN;
 #pragma unroll
                         for (int i = 0; i < BN; ++i)
                             s[i] = (i <= c_hi && (i >= c_lo || i < c_sink)) ? s[i] : -INFINITY;
@@ -923,6 +940,14 @@ PrefillGeometry prefill_geometry(int window) {
     return {LongCfg::CTA_TOK, LongCfg::BN, LongCfg::V_BOX, LongCfg::ASYNC_EPI};
 }
 
+template <bool SINK>
+static SinkMaps<SINK> sink_maps(const SinkMaps<true> &maps) {
+    if constexpr (SINK)
+        return maps;
+    else
+        return {};
+}
+
 // Each kernel instantiation opts in to its shared memory once per device (a
 // driver call that need not be repeated on every launch).
 template <class C, class Plan>
@@ -938,7 +963,8 @@ static cudaError_t launch_cfg(const PrefillLaunch &L, const Plan &plan, int dev,
     const long long work = static_cast<long long>(plan.n_items) * plan.hkv;
     const unsigned grid = static_cast<unsigned>(work < num_sms ? work : num_sms);
     gdla_prefill_kernel<C, Plan><<<grid, C::NUM_THREADS, C::SMEM_BYTES, stream>>>(
-        L.tm_qs, L.tm_qn, L.tm_k, L.tm_v, L.tm_gate, L.tm_lam, L.tm_out, L.lambda, L.gate, L.out, L.bwd, plan);
+        L.tm_qs, L.tm_qn, L.tm_k, L.tm_v, L.tm_gate, L.tm_lam, L.tm_out, sink_maps<C::SINK>(L.sink), L.lambda, L.gate,
+        L.out, L.bwd, plan);
     return cudaPeekAtLastError();
 }
 

@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(pbq::NUM_THREADS, 1)
 gdla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_constant__ CUtensorMap tm_qn,
                    const __grid_constant__ CUtensorMap tm_dhs, const __grid_constant__ CUtensorMap tm_dhn,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const float *__restrict__ stats, __nv_bfloat16 *__restrict__ dq_sig,
+                   const __grid_constant__ SinkMaps<SINK> sink, const float *__restrict__ stats,
+                   __nv_bfloat16 *__restrict__ dq_sig,
                    __nv_bfloat16 *__restrict__ dq_noise, const __grid_constant__ Plan plan) {
     using namespace pbq;
     extern __shared__ uint8_t smem_raw[];
@@ -134,11 +135,8 @@ gdla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_const
     const int n_work = plan.n_items * hkv;
 
     struct Item {
-        int group, s0, L, t0, kv_lo, n_sink, n_tiles;
-        __device__ __forceinline__ int key0(int k) const {  // first key of key tile k
-            if (SINK) return k < n_sink ? k * pbq::BN : kv_lo + (k - n_sink) * pbq::BN;
-            return kv_lo + k * pbq::BN;
-        }
+        int group, s0, L, t0, kv_lo, n_tiles;
+        int pre;  // columns of sinks before the window's keys
     };
     auto item_at = [&](int w) {
         Item it;
@@ -149,13 +147,13 @@ gdla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_const
         it.L = plan.seq_len[seq];
         it.t0 = static_cast<int>(code & kItemTileMask) * TOK;
         it.kv_lo = (window > 0) ? max(0, it.t0 - window + 1) : 0;
-        it.n_sink = 0;
+        it.pre = 0;
         if constexpr (SINK) {
-            const SinkTiles st = sink_tiles(it.kv_lo, plan.sinks, BN);
-            it.n_sink = st.n_sink;
-            it.kv_lo = st.kv_lo;
+            const SinkRun run = sink_run(it.kv_lo, plan.sinks);
+            it.pre = run.pre;
+            it.kv_lo = run.kv_lo;
         }
-        it.n_tiles = max(1, it.n_sink + (min(it.L, it.t0 + TOK) - it.kv_lo + BN - 1) / BN);
+        it.n_tiles = max(1, (it.pre + min(it.L, it.t0 + TOK) - it.kv_lo + BN - 1) / BN);
         return it;
     };
 
@@ -225,8 +223,24 @@ gdla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_const
                         break;
                     }
                     mbar_arrive_expect_tx(kv_full + st, STAGE);
-                    const int row = it.s0 + it.key0(k);
+                    int row = it.s0 + it.kv_lo - it.pre + k * BN;
                     uint8_t *sb = smem + OFF_KV + st * STAGE;
+                    if constexpr (SINK) {
+                        const int n_sink = it.pre - k * BN;  // sink rows from this tile on
+                        if (n_sink >= BN) row = it.s0 + k * BN;
+                        if (n_sink > 0 && n_sink < BN) {  // sinks and window in one tile
+                            for (int c = 0; c < 5; ++c) {
+                                const CUtensorMap *first = c < 3 ? &sink.k_sink : &sink.v_sink;
+                                const CUtensorMap *rest = c < 3 ? &sink.k_rest : &sink.v_rest;
+                                const int d = (c < 3 ? c : c - 3) * 64;
+                                tma_load_3d(sb + c * KV_CHUNK, first, kv_full + st, d, it.group, it.s0 + k * BN);
+                                tma_load_3d(sb + c * KV_CHUNK + n_sink * 128, rest, kv_full + st, d, it.group,
+                                            it.s0 + it.kv_lo);
+                            }
+                            issued = kv + 1;
+                            continue;
+                        }
+                    }
                     for (int c = 0; c < 3; ++c) tma_load_3d(sb + c * KV_CHUNK, &tm_k, kv_full + st, c * 64, it.group, row);
                     for (int c = 0; c < 2; ++c)
                         tma_load_3d(sb + K_STAGE + c * KV_CHUNK, &tm_v, kv_full + st, c * 64, it.group, row);
@@ -346,12 +360,12 @@ gdla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_const
                 const uint32_t s_addr = lane_base + S_COL0 + b * BUF_COLS + 32 * half;
                 uint32_t sr[32], dr[32];
                 tmem_ld32x2(s_addr, lane_base + DP_COL0 + b * BUF_COLS + 32 * half, sr, dr);
-                const int u0 = it.key0(k) + 32 * half;
+                const int u0 = it.kv_lo - it.pre + k * BN + 32 * half;
                 // bit c: key u0 + c is visible to this row (c <= t - u0, and c > t - window - u0)
                 uint32_t vm;
-                if constexpr (SINK) {  // or u0 + c is one of the sinks
+                if constexpr (SINK) {  // or the column is one of the sinks'
                     const auto low = [](int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); };
-                    vm = row_ok ? low(t - u0 + 1) & (~low(t - window - u0 + 1) | low(plan.sinks - u0)) : 0u;
+                    vm = row_ok ? low(t - u0 + 1) & (~low(t - window - u0 + 1) | low(plan.sinks - k * BN - 32 * half)) : 0u;
                 } else {
                     const int hi = min(31, t - u0);
                     const int lo = (window > 0) ? max(0, t - window - u0 + 1) : 0;
@@ -862,7 +876,7 @@ static cudaError_t launch_dq_sized(const BwdLaunch &L, const Plan &plan, cudaStr
     const long long work = static_cast<long long>(plan.n_items) * plan.hkv;
     const unsigned grid = static_cast<unsigned>(work < num_sms ? work : num_sms);
     gdla_bwd_dq_kernel<Plan, SINK><<<grid, pbq::NUM_THREADS, pbq::SMEM_BYTES, stream>>>(
-        L.tm_qs, L.tm_qn, L.tm_dhs, L.tm_dhn, L.tm_k64, L.tm_v64, L.stats, L.dq_sig, L.dq_noise, plan);
+        L.tm_qs, L.tm_qn, L.tm_dhs, L.tm_dhn, L.tm_k64, L.tm_v64, sink_maps<SINK>(L.sink64), L.stats, L.dq_sig, L.dq_noise, plan);
     return cudaPeekAtLastError();
 }
 
