@@ -399,10 +399,6 @@ def attn_decode_latent(q_abs_sig, q_abs_noise, ckv, cu_seqlens_k, max_seqlen_k, 
 
 # The paged-cache calls are made once per layer and token, so their checks are one
 # combined test per tensor, which hands back the pointer; what failed is worked out only then.
-def _launch_device(stream):
-    return torch.cuda.current_device() if stream is None else stream.device.index
-
-
 def _dense(t, name, dtype, shape, dev):
     """The pointer of a contiguous tensor of this type and shape on CUDA device ``dev``."""
     if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == dev
@@ -410,16 +406,19 @@ def _dense(t, name, dtype, shape, dev):
         return t.data_ptr()
     _check(t, name, dtype, shape)
     if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's launch stream on cuda:{dev}")
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, k_pages on cuda:{dev}")
     return t.data_ptr()
 
 
-def _cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev):
-    """The paged cache's own arguments, checked: (sizes, pointers)."""
+def _cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, stream):
+    """The paged cache's own arguments and the launch stream, checked: (device, sizes, pointers)."""
     if not isinstance(k_pages, torch.Tensor) or not isinstance(block_table, torch.Tensor):
         raise TypeError("k_pages and block_table must be torch.Tensors")
     if k_pages.dim() != 4 or block_table.dim() != 2:
         raise ValueError("expected k_pages [pages, H, page_size, 192] and block_table [batch, pages per sequence]")
+    dev = k_pages.get_device()
+    if dev < 0:
+        raise ValueError("k_pages must be on a CUDA device")
     np_, hkv, ps, _ = k_pages.shape
     b, width = block_table.shape
     dt = k_pages.dtype
@@ -438,7 +437,10 @@ def _cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev):
     vp = _dense(v_pages, "v_pages", dt, (np_, hkv, ps, DV), dev)
     bt = _dense(block_table, "block_table", torch.int32, (b, width), dev)
     sl = _dense(seqlens_k, "seqlens_k", torch.int32, (b,), dev)
-    return kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl
+    sdev = torch.cuda.current_device() if stream is None else stream.device.index
+    if sdev != dev:
+        raise ValueError(f"the tensors are on cuda:{dev} but the launch stream is on cuda:{sdev}")
+    return dev, kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl
 
 
 def _rows(t, name, shape, dev):
@@ -454,7 +456,7 @@ def _rows(t, name, shape, dev):
         if not t.is_cuda:
             raise ValueError(f"{name} must be on a CUDA device")
         if t.get_device() != dev:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's launch stream on cuda:{dev}")
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, k_pages on cuda:{dev}")
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}: its last dimension must be contiguous")
@@ -479,10 +481,9 @@ def cache_append(k_nope, k_rope, v, k_pages, v_pages, block_table, cu_seqlens_ne
     b, which then holds seqlens_k[b] tokens. ``rotate`` turns k_rope to each token's
     position on the way. Pages and scales are updated in place.
     """
-    dev = _launch_device(stream)
-    kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl = _cache(k_pages, v_pages, k_scale, v_scale, block_table,
-                                                                  seqlens_k, dev)
-    n = v.shape[0]
+    dev, kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl = _cache(k_pages, v_pages, k_scale, v_scale, block_table,
+                                                                       seqlens_k, stream)
+    n = v.shape[0] if isinstance(v, torch.Tensor) and v.dim() else -1
     kn, kn_t, kn_h = _rows(k_nope, "k_nope", (n, hkv, DQK - DR), dev)
     kr, kr_t, _ = _rows(k_rope, "k_rope", (n, DR), dev)
     vv, v_t, v_h = _rows(v, "v", (n, hkv, DV), dev)
@@ -509,9 +510,8 @@ def attn_decode_paged(q_sig, q_noise, k_pages, v_pages, block_table, seqlens_k, 
     position first. ``workspace`` (uint8 CUDA tensor) is allocated here when not given.
     Returns out [B, 4H, 128] bf16.
     """
-    dev = _launch_device(stream)
-    kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl = _cache(k_pages, v_pages, k_scale, v_scale, block_table,
-                                                                  seqlens_k, dev)
+    dev, kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl = _cache(k_pages, v_pages, k_scale, v_scale, block_table,
+                                                                       seqlens_k, stream)
     hs = GROUP * hkv
     qs = _dense(q_sig, "q_sig", torch.bfloat16, (b, hs, DQK), dev)
     qn = _dense(q_noise, "q_noise", torch.bfloat16, (b, hkv, DQK), dev)
@@ -532,7 +532,7 @@ def attn_decode_paged(q_sig, q_noise, k_pages, v_pages, block_table, seqlens_k, 
     else:
         _check_workspace(workspace)
         if workspace.get_device() != dev:
-            raise ValueError(f"workspace is on cuda:{workspace.get_device()}, the call's launch stream on cuda:{dev}")
+            raise ValueError(f"workspace is on cuda:{workspace.get_device()}, k_pages on cuda:{dev}")
         st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
     if st != 0:
         raise GDLAError(st, "gdla_attn_decode_paged")
