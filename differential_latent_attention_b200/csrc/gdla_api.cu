@@ -126,13 +126,20 @@ struct TileItem {
     int qt;
 };
 
+// How the dK, dV items of a call with sinks are cut, and where each sequence's partials begin (-1: it has none).
+struct DkvSplits {
+    DkvSplit split{1, 0, 32};
+    std::vector<int> part, tile_part;
+    long long slots = 0, tile_slots = 0;
+};
+
 // Every (sequence, unit) with its cost, heaviest first, in plans of at most
 // kPlanMaxItems units and kPlanMaxSeqs sequences; launch(plan) for each. A sequence of
-// length L has units(L) of them, unit u costs cost(L, u) and is item index(L, u); part[b]
-// (empty: -1) goes with the sequence. Returns false on the first failed launch.
+// length L has units(L) of them, unit u costs cost(L, u) and is item index(L, u); the partial
+// slots of `parts` (empty: none) go with the sequences. Returns false on the first failed launch.
 template <class Units, class Cost, class Index, class Launch>
-bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int sinks, const std::vector<int> &part,
-               Units units, Cost cost, Index index, Launch launch) {
+bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int sinks, const DkvSplits &parts, Units units,
+               Cost cost, Index index, Launch launch) {
     std::vector<TileItem> items;
     std::vector<int> seq_start(batch);
     long long s0 = 0;
@@ -141,7 +148,10 @@ bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int sinks
         const int L = seqlens[b];
         s0 += L;
         const int nu = units(L);
-        for (int u = 0; u < nu; ++u) items.push_back({cost(L, u), b, u});
+        for (int u = 0; u < nu; ++u) {
+            const int c = cost(L, u);
+            if (c > 0) items.push_back({c, b, u});
+        }
     }
     std::stable_sort(items.begin(), items.end(), [](const TileItem &a, const TileItem &b) {
         if (a.cost != b.cost) return a.cost > b.cost;
@@ -157,6 +167,7 @@ bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int sinks
         P.hkv = hkv;
         P.window = window;
         P.sinks = sinks;
+        P.split = parts.split;
         int n_seq = 0;
         std::vector<int> used;
         while (pos < items.size() && P.n_items < kPlanMaxItems) {
@@ -166,7 +177,8 @@ bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int sinks
                 local[it.seq] = n_seq;
                 P.seq_start[n_seq] = seq_start[it.seq];
                 P.seq_len[n_seq] = seqlens[it.seq];
-                P.part[n_seq] = part.empty() ? -1 : part[it.seq];
+                P.part[n_seq] = parts.part.empty() ? -1 : parts.part[it.seq];
+                P.tile_part[n_seq] = parts.tile_part.empty() ? -1 : parts.tile_part[it.seq];
                 used.push_back(it.seq);
                 ++n_seq;
             }
@@ -184,7 +196,7 @@ bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int sinks
 template <class Cost, class Launch>
 bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int sinks, int unit_tokens, Cost cost,
                Launch launch) {
-    return run_plans(batch, seqlens, hkv, window, sinks, {},
+    return run_plans(batch, seqlens, hkv, window, sinks, DkvSplits(),
                      [=](int L) { return (L + unit_tokens - 1) / unit_tokens; }, cost,
                      [](int, int u) { return static_cast<uint32_t>(u); }, launch);
 }
@@ -213,15 +225,16 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace of the backward: dH of the signal and noise heads (bf16) and the row statistics.
 struct BwdWorkspace {
-    size_t dh_sig, dh_noise, stats, part, total;
+    size_t dh_sig, dh_noise, stats, part, tile_part, total;
 };
-BwdWorkspace bwd_workspace(long long n, int hkv, long long part_slots = 0, int sinks = 0) {
+BwdWorkspace bwd_workspace(long long n, int hkv, const DkvSplits &parts = DkvSplits(), int sinks = 0) {
     BwdWorkspace w;
     w.dh_sig = 0;
     w.dh_noise = align256(static_cast<size_t>(n) * 4 * hkv * 128 * 2);
     w.stats = w.dh_noise + align256(static_cast<size_t>(n) * hkv * 128 * 2);
     w.part = w.stats + align256(static_cast<size_t>(n) * hkv * kBwdStats * 4);
-    w.total = w.part + align256(static_cast<size_t>(part_slots) * hkv * sinks * (192 + 128) * 4);
+    w.tile_part = w.part + align256(static_cast<size_t>(parts.slots) * hkv * sinks * (192 + 128) * 4);
+    w.total = w.tile_part + align256(static_cast<size_t>(parts.tile_slots) * hkv * kBwdKeyTile * (192 + 128) * 4);
     return w;
 }
 
@@ -262,18 +275,41 @@ gdla_status_t check_sinks(int longest, int *window, int *sinks) {
     return GDLA_OK;
 }
 
-// First partial slot of each sequence with sink chunks (-1: none); returns the slots in all.
-long long sink_slots(int batch, const int32_t *seqlens, int window, int sinks, std::vector<int> *part) {
-    long long slots = 0;
-    if (part) part->assign(batch, -1);
-    if (sinks <= 0) return 0;
+// Key tiles of all sequences fill the card by themselves from one item per SM on; with fewer each is cut
+// into as many items as make one round of the card, of 8 steps at least (loading a tile's keys and writing its
+// partials cost about three).
+DkvSplits dkv_splits(int batch, const int32_t *seqlens, int hkv, int window, int sinks) {
+    DkvSplits p;
+    if (sinks <= 0) return p;
+    long long tiles = 0;
+    int most = 0;
     for (int b = 0; b < batch; ++b) {
-        const int n = seqlens[b] > 0 ? bwd_sink_chunks(seqlens[b], window) : 0;
-        if (n == 0) continue;
-        if (part) (*part)[b] = static_cast<int>(slots);
-        slots += n + 1;
+        if (seqlens[b] == 0) continue;
+        tiles += (seqlens[b] + kBwdKeyTile - 1) / kBwdKeyTile;
+        most = std::max(most, bwd_tile_steps(seqlens[b], 0, window));
     }
-    return slots;
+    if (tiles == 0) return p;
+    const int chunks = static_cast<int>(std::min<long long>(kPlanSms / (tiles * hkv), most / 8));
+    if (chunks > 1) {
+        p.split.chunk_steps = (most + chunks - 1) / chunks;
+        p.split.chunks = (most + p.split.chunk_steps - 1) / p.split.chunk_steps;
+        p.split.sink_steps = std::min(32, p.split.chunk_steps);
+    }
+    p.part.assign(batch, -1);
+    p.tile_part.assign(batch, -1);
+    for (int b = 0; b < batch; ++b) {
+        if (seqlens[b] == 0) continue;
+        const int n = bwd_sink_chunks(seqlens[b], window, p.split.sink_steps);
+        if (n > 0) {
+            p.part[b] = static_cast<int>(p.slots);
+            p.slots += n + 1;
+        }
+        if (p.split.chunks > 1) {
+            p.tile_part[b] = static_cast<int>(p.tile_slots);
+            p.tile_slots += static_cast<long long>((seqlens[b] + kBwdKeyTile - 1) / kBwdKeyTile) * p.split.chunks;
+        }
+    }
+    return p;
 }
 
 }  // namespace
@@ -396,9 +432,8 @@ static gdla_status_t attn_bwd(const void *q_sig, const void *q_noise, const void
         !aligned16(dk) || !aligned16(dv) || !aligned16(dlambda) || !aligned16(dgate))
         return GDLA_ERR_INVALID_ARG;
     const int hkv = num_kv_heads;
-    std::vector<int> part;
-    const long long slots = sink_slots(batch, seqlens, window, sinks, &part);
-    const BwdWorkspace ws = bwd_workspace(n_total, hkv, slots, sinks);
+    const DkvSplits parts = dkv_splits(batch, seqlens, hkv, window, sinks);
+    const BwdWorkspace ws = bwd_workspace(n_total, hkv, parts, sinks);
     if (workspace == nullptr || workspace_bytes < ws.total || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return GDLA_ERR_WORKSPACE;
     uint8_t *wsb = static_cast<uint8_t *>(workspace);
@@ -463,34 +498,48 @@ static gdla_status_t attn_bwd(const void *q_sig, const void *q_noise, const void
             return GDLA_ERR_CUDA;
         return GDLA_OK;
     }
-    // with sinks: the key tiles, then the chunks of later rows that see the sinks alone
+    // with sinks: the key tiles (or their parts), and the chunks of later rows that see the sinks alone
     B.part = reinterpret_cast<float *>(wsb + ws.part);
-    auto tiles = [](int L) { return (L + kBwdKeyTile - 1) / kBwdKeyTile; };
-    auto units = [=](int L) { return L > 0 ? tiles(L) + bwd_sink_chunks(L, window) : 0; };
-    auto cost = [=](int L, int u) {
-        if (u < tiles(L)) return bwd_tile_steps(L, u * kBwdKeyTile, window);
-        const int first = bwd_tile_steps(L, 0, window) + (u - tiles(L)) * kBwdSinkSteps;
-        return std::min(kBwdSinkSteps, (L + kBwdStepTokens - 1) / kBwdStepTokens - first);
+    B.tile_part = reinterpret_cast<float *>(wsb + ws.tile_part);
+    const DkvSplit split = parts.split;
+    auto tile_items = [=](int L) { return (L + kBwdKeyTile - 1) / kBwdKeyTile * split.chunks; };
+    auto units = [=](int L) { return L > 0 ? tile_items(L) + bwd_sink_chunks(L, window, split.sink_steps) : 0; };
+    auto cost = [=](int L, int u) {  // steps; 0 where a tile has fewer parts than the longest
+        if (u < tile_items(L)) {
+            const int steps = bwd_tile_steps(L, u / split.chunks * kBwdKeyTile, window);
+            if (split.chunks == 1) return steps;
+            return std::max(0, std::min(split.chunk_steps, steps - u % split.chunks * split.chunk_steps));
+        }
+        const int first = bwd_tile_steps(L, 0, window) + (u - tile_items(L)) * split.sink_steps;
+        return std::min(split.sink_steps, (L + kBwdStepTokens - 1) / kBwdStepTokens - first);
     };
     auto index = [=](int L, int u) {
-        return u < tiles(L) ? static_cast<uint32_t>(u) : kItemSinkChunk | static_cast<uint32_t>(u - tiles(L));
+        return u < tile_items(L) ? static_cast<uint32_t>(u) : kItemSinkChunk | static_cast<uint32_t>(u - tile_items(L));
     };
-    if (!run_plans(batch, seqlens, hkv, window, sinks, part, units, cost, index,
+    if (!run_plans(batch, seqlens, hkv, window, sinks, parts, units, cost, index,
                    [&](const PrefillPlan &P) { return launch_bwd_dkv(B, P, st) == cudaSuccess; }))
         return GDLA_ERR_CUDA;
     std::unique_ptr<BwdSinkSum> sum(new BwdSinkSum);
     sum->part = B.part;
+    sum->tile_part = B.tile_part;
     sum->dk = B.dk;
     sum->dv = B.dv;
     sum->hkv = hkv;
     sum->sinks = sinks;
+    sum->window = window;
+    sum->split = split;
     sum->n_seqs = 0;
+    sum->row0[0] = 0;
     long long s0 = 0;
     for (int b = 0; b < batch; ++b) {
-        if (part[b] >= 0) {
-            sum->start[sum->n_seqs] = static_cast<int>(s0);
-            sum->slot[sum->n_seqs] = part[b];
-            sum->count[sum->n_seqs++] = bwd_sink_chunks(seqlens[b], window) + 1;
+        const int rows = split.chunks > 1 ? seqlens[b] : parts.part[b] >= 0 ? sinks : 0;
+        if (rows > 0) {
+            const int q = sum->n_seqs++;
+            sum->start[q] = static_cast<int>(s0);
+            sum->len[q] = seqlens[b];
+            sum->slot[q] = parts.part[b];
+            sum->tile_slot[q] = parts.tile_part[b];
+            sum->row0[q + 1] = sum->row0[q] + rows;
         }
         s0 += seqlens[b];
         if (sum->n_seqs > 0 && (sum->n_seqs == kSinkSumMaxSeqs || b == batch - 1)) {
@@ -508,7 +557,7 @@ size_t gdla_attn_bwd_sinks_workspace_bytes(int batch, const int32_t *seqlens, in
     if (check_seqlens(batch, seqlens, num_kv_heads, &n_total, &longest) != GDLA_OK ||
         check_sinks(longest, &window, &sinks) != GDLA_OK)
         return 0;
-    return bwd_workspace(n_total, num_kv_heads, sink_slots(batch, seqlens, window, sinks, nullptr), sinks).total;
+    return bwd_workspace(n_total, num_kv_heads, dkv_splits(batch, seqlens, num_kv_heads, window, sinks), sinks).total;
 }
 
 gdla_status_t gdla_attn_bwd(const void *q_sig, const void *q_noise, const void *k, const void *v,

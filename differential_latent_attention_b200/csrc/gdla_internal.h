@@ -58,6 +58,11 @@ struct SinkMaps<true> {
     CUtensorMap k_sink, k_rest, v_sink, v_rest;
 };
 
+// How the dK, dV kernel with sinks cuts its items (see the backward below).
+struct DkvSplit {
+    int chunks, chunk_steps, sink_steps;
+};
+
 // Passed by value (kernel parameters): the q-tiles of one launch, heaviest
 // first. The host builds the largest form and launches the smallest capacity
 // that holds the plan, so a launch carries ~3.3 KB, ~8.7 KB or ~26.6 KB.
@@ -72,7 +77,9 @@ struct PrefillPlanT {
     int n_seqs;
     int seq_start[MAX_SEQS];  // packed row of each sequence's first token
     int seq_len[MAX_SEQS];
-    int part[MAX_SEQS];       // dkv with sinks: first partial slot of the sequence, -1 for none
+    DkvSplit split;           // dkv with sinks
+    int part[MAX_SEQS];       // .. the sequence's first sink partial, -1 for none
+    int tile_part[MAX_SEQS];  // .. its first tile's first partial where tiles are cut
     uint32_t items[MAX_ITEMS];  // (local sequence << kItemSeqShift) | CTA block index
 };
 using PrefillPlan = PrefillPlanT<kPlanMaxItems, kPlanMaxSeqs>;
@@ -121,29 +128,35 @@ struct BwdLaunch {
     const float *stats;
     __nv_bfloat16 *dq_sig, *dq_noise, *dk, *dv;
     float *part;                    // sinks: fp32 partials of dK | dV, [slot][KV head][sink][320]
+    float *tile_part;               // .. of cut tiles, [slot][KV head][128][320]
 };
-// dK, dV of the sinks: every later token of the sequence sees them, so the rows past the
-// first key tile's window are cut into chunks of kBwdSinkSteps steps, an item each, and
-// the items' partial sums are added up in order by a last kernel.
-constexpr int kBwdSinkSteps = 32;
+// dK, dV with sinks. Every later token of a sequence sees them, so the rows past the first key
+// tile's window are cut into chunks of sink_steps steps, an item each, whose sums for the
+// sinks leave in fp32 and are added up in order by a last kernel. Where the key tiles are too few
+// for the card, the tiles' own steps are cut the same way: `chunks` items per tile of chunk_steps
+// steps, every row by way of partials. (5 sequences of 2,661 tokens, 2 heads, window 333: 46 items of
+// up to 39 steps took 57 us.)
 constexpr uint32_t kItemSinkChunk = 1u << 19;  // in a dkv item's tile index: sink chunk, not key tile
 // Steps of the key tile at u0, and sink chunks behind those of the first tile.
 __host__ __device__ __forceinline__ int bwd_tile_steps(int L, int u0, int window) {
     const int t_end = (window > 0 && window < L - u0 - (kBwdKeyTile - 1)) ? u0 + kBwdKeyTile - 1 + window : L;
     return (t_end - u0 + kBwdStepTokens - 1) / kBwdStepTokens;
 }
-__host__ __device__ __forceinline__ int bwd_sink_chunks(int L, int window) {
+__host__ __device__ __forceinline__ int bwd_sink_chunks(int L, int window, int sink_steps) {
     const int left = (L + kBwdStepTokens - 1) / kBwdStepTokens - bwd_tile_steps(L, 0, window);
-    return left > 0 ? (left + kBwdSinkSteps - 1) / kBwdSinkSteps : 0;
+    return left > 0 ? (left + sink_steps - 1) / sink_steps : 0;
 }
 constexpr int kSinkSumMaxSeqs = 256;
-struct BwdSinkSum {  // one launch's sequences with sink chunks
-    const float *part;
+struct BwdSinkSum {  // the sequences of one launch of the last kernel
+    const float *part, *tile_part;
     __nv_bfloat16 *dk, *dv;
-    int hkv, sinks, n_seqs;
-    int start[kSinkSumMaxSeqs];  // packed row of the sequence's first token
-    int slot[kSinkSumMaxSeqs];   // its first partial
-    int count[kSinkSumMaxSeqs];  // its partials
+    int hkv, sinks, n_seqs, window;
+    DkvSplit split;
+    int row0[kSinkSumMaxSeqs + 1];  // first row (key) of the launch that is the sequence's
+    int start[kSinkSumMaxSeqs];     // packed row of its first token
+    int len[kSinkSumMaxSeqs];
+    int slot[kSinkSumMaxSeqs];      // its first sink partial (-1: none), and its first tile's first partial
+    int tile_slot[kSinkSumMaxSeqs];
 };
 cudaError_t launch_bwd_sink_sum(const BwdSinkSum &sum, cudaStream_t stream);
 cudaError_t launch_bwd_dq(const BwdLaunch &launch, const PrefillPlan &plan, cudaStream_t stream);

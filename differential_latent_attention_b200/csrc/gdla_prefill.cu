@@ -269,32 +269,44 @@ __device__ __forceinline__ void epi_chunk_staged(const uint32_t (&o)[32], float 
 // with dH rounded to bf16 (the operand the gradient kernels multiply) and the
 // row statistics lse2 = m + log2(l) (so P = exp2(s log2(e)/sqrt(192) - lse2))
 // and rowsum(dH * H) taken with that rounded dH.
+// The rows of gate and dout are read a 32-column chunk ahead: the first before the wait for the item's last
+// product, each next one while a chunk is computed.
+struct BwdRow {
+    uint4 g[4], go[4];
+};
+__device__ __forceinline__ void epi_bwd_fetch(bool sig, size_t srow, const __nv_bfloat16 *__restrict__ gate,
+                                              const __nv_bfloat16 *__restrict__ dout, int ch, BwdRow &row) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        row.g[i] = row.go[i] = make_uint4(0, 0, 0, 0);
+        if (sig) {
+            row.g[i] = __ldg(reinterpret_cast<const uint4 *>(gate + srow * DV + ch * 32) + i);
+            row.go[i] = __ldg(reinterpret_cast<const uint4 *>(dout + srow * DV + ch * 32) + i);
+        }
+    }
+}
 __device__ __forceinline__ void epi_backward(uint32_t o_addr, float l_run, float m_run, bool is_sig, bool tok_valid,
-                                             int lane, int hsrc, size_t tok, int hs, int hkv, int group,
-                                             const float *__restrict__ lambda, const __nv_bfloat16 *__restrict__ gate,
+                                             int lane, int hsrc, size_t tok, int hs, int hkv, int group, float lam,
+                                             BwdRow &next, const __nv_bfloat16 *__restrict__ gate,
                                              const BwdIO &bwd) {
     const bool sig = is_sig && tok_valid;
     const bool noi = lane >= 24 && lane < 30 && tok_valid;
     const size_t srow = tok * hs + 4 * group + (lane & 3);
     const size_t nrow = tok * hkv + group;
     const float inv_l = (l_run > 0.f) ? 1.f / l_run : 0.f;
-    const float lam = sig ? __ldg(lambda + srow) : 0.f;
     const int nsrc = ((lane - 24) * 4) & 31;  // noise lane 24+i: the first signal lane of token i
     float dl = 0.f, drow = 0.f;
 #pragma unroll 1
     for (int ch = 0; ch < DV / 32; ++ch) {
         uint32_t o[32], g[16], go[16];
-        tmem_ld32(o_addr + ch * 32, o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint4 a = make_uint4(0, 0, 0, 0), c = a;
-            if (sig) {
-                a = __ldg(reinterpret_cast<const uint4 *>(gate + srow * DV + ch * 32) + i);
-                c = __ldg(reinterpret_cast<const uint4 *>(bwd.dout + srow * DV + ch * 32) + i);
-            }
+            const uint4 a = next.g[i], c = next.go[i];
             g[4 * i] = a.x, g[4 * i + 1] = a.y, g[4 * i + 2] = a.z, g[4 * i + 3] = a.w;
             go[4 * i] = c.x, go[4 * i + 1] = c.y, go[4 * i + 2] = c.z, go[4 * i + 3] = c.w;
         }
+        if (ch + 1 < DV / 32) epi_bwd_fetch(sig, srow, gate, bwd.dout, ch + 1, next);
+        tmem_ld32(o_addr + ch * 32, o);
         uint32_t w_dgate[16], w_dh[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -884,14 +896,17 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
                     epi_chunk(o, inv_l, lam, gw[ch - 2], hsrc, valid, wide, out + row * DV + ch * 32);
                 }
             } else if constexpr (C::EPI == EPI_BWD) {
+                BwdRow first;
+                epi_bwd_fetch(valid, row, gate, bwd.dout, 0, first);
+                const float lam = valid ? __ldg(lambda + row) : 0.f;
                 if (!__all_sync(0xffffffffu, mbar_wait(o_final + x, n_item & 1, abort_flag, ERR_SITE_PREFILL | 9))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const size_t tok = static_cast<size_t>(it.s0 + t);
-                epi_backward(o_addr, l_run, m_run, is_sig, t < it.L, lane, hsrc, tok, hs, hkv, it.group, lambda, gate,
-                             bwd);
+                epi_backward(o_addr, l_run, m_run, is_sig, t < it.L, lane, hsrc, tok, hs, hkv, it.group, lam, first,
+                             gate, bwd);
             } else {
                 // Signal rows fetch their gate row and lambda before waiting for the last PV.
                 uint32_t gw[DV / 32][16];

@@ -467,7 +467,8 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
                     const __grid_constant__ CUtensorMap tm_dhs, const __grid_constant__ CUtensorMap tm_dhn,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_stats, __nv_bfloat16 *__restrict__ dk,
-                    __nv_bfloat16 *__restrict__ dv, float *__restrict__ part, const __grid_constant__ Plan plan) {
+                    __nv_bfloat16 *__restrict__ dv, float *__restrict__ part, float *__restrict__ tile_part,
+                    const __grid_constant__ Plan plan) {
     using namespace pbk;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -492,8 +493,9 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
     // With sinks: items of the first key tile's sinks over a later chunk of steps too.
     struct Item {
         int group, s0, L, u0, step0, n_steps;
-        int slot;  // partial slot of this item's sink rows, -1: every row goes straight out
-        bool chunk;
+        int slot;       // partial slot of this item's sink rows, -1: none
+        int tile_slot;  // partial slot of all its rows (a cut tile), -1: none
+        bool chunk;     // rows of a later chunk: the sinks alone
     };
     auto item_at = [&](int w) {
         Item it;
@@ -503,17 +505,22 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
         it.s0 = plan.seq_start[seq];
         it.L = plan.seq_len[seq];
         it.step0 = 0;
-        it.slot = -1;
+        it.slot = it.tile_slot = -1;
         it.chunk = false;
         if constexpr (SINK) {
             it.chunk = (code & kItemSinkChunk) != 0;
-            it.u0 = it.chunk ? 0 : static_cast<int>(code & (kItemSinkChunk - 1)) * BK;
+            const int j = static_cast<int>(code & (kItemSinkChunk - 1)), chunks = plan.split.chunks;
+            const int tile = it.chunk ? 0 : j / chunks;
+            it.u0 = tile * BK;
             it.n_steps = bwd_tile_steps(it.L, it.u0, window);
             if (it.chunk) {
-                const int j = static_cast<int>(code & (kItemSinkChunk - 1));
-                it.step0 = it.n_steps + j * kBwdSinkSteps;
-                it.n_steps = min(kBwdSinkSteps, (it.L + HT - 1) / HT - it.step0);
+                it.step0 = it.n_steps + j * plan.split.sink_steps;
+                it.n_steps = min(plan.split.sink_steps, (it.L + HT - 1) / HT - it.step0);
                 it.slot = plan.part[seq] + 1 + j;
+            } else if (chunks > 1) {
+                it.step0 = (j - tile * chunks) * plan.split.chunk_steps;
+                it.n_steps = min(plan.split.chunk_steps, it.n_steps - it.step0);
+                it.tile_slot = plan.tile_part[seq] + j;
             } else if (it.u0 == 0) {
                 it.slot = plan.part[seq];
             }
@@ -778,11 +785,15 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
             if (!__all_sync(0xffffffffu, mbar_wait(dkv_final, n_item & 1, abort_flag, ERR_SITE_BWD | 17))) break;
             tc_fence_after();
             const size_t krow = static_cast<size_t>(it.s0 + u) * hkv + it.group;
-            // sink rows of a sequence with chunks leave as fp32 partials, other rows of a chunk not at all
-            const bool to_part = SINK && it.slot >= 0 && u < plan.sinks;
+            // sink rows of a sequence with chunks, and every row of a cut tile, leave as fp32 partials; other
+            // rows of a chunk not at all
+            const bool cut = SINK && it.tile_slot >= 0;
+            const bool to_part = (cut && key_ok) || (SINK && it.slot >= 0 && u < plan.sinks);
             const bool to_out = key_ok && !to_part && !(SINK && it.chunk);
             float *prow = part;
-            if (to_part)
+            if (cut)
+                prow = tile_part + ((static_cast<size_t>(it.tile_slot) * hkv + it.group) * BK + kl) * (DQK + DV);
+            else if (to_part)
                 prow += ((static_cast<size_t>(it.slot) * hkv + it.group) * plan.sinks + u) * (DQK + DV);
             const auto put_part = [&](const uint32_t (&o)[32], float f, int col) {
 #pragma unroll
@@ -836,25 +847,52 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
 // ------------------------------------------------------------------------------
 // Host side
 // ------------------------------------------------------------------------------
-// dK and dV of the sinks: the partials of a (sequence, KV head, sink) added up in slot order,
-// one thread per dim.
+// dK and dV of the rows that left as partials: 80 threads per (key, KV head), four dims each, four of them a
+// block. A cut tile's partials in the order of its steps (or, of an uncut first tile, its sinks' own partial), then
+// the later chunks'.
 __global__ void __launch_bounds__(320) gdla_bwd_sink_sum_kernel(const __grid_constant__ BwdSinkSum p) {
-    const int u = blockIdx.x % p.sinks, group = (blockIdx.x / p.sinks) % p.hkv, q = blockIdx.x / (p.sinks * p.hkv);
-    const int d = threadIdx.x;
-    const size_t step = static_cast<size_t>(p.hkv) * p.sinks * 320;
-    const float *src = p.part + (static_cast<size_t>(p.slot[q]) * p.hkv + group) * p.sinks * 320 + u * 320 + d;
-    float sum = 0.f;
-    for (int i = 0; i < p.count[q]; ++i) sum += src[i * step];
-    const size_t row = static_cast<size_t>(p.start[q] + u) * p.hkv + group;
-    if (d < 192)
-        p.dk[row * 192 + d] = __float2bfloat16_rn(sum);
-    else
-        p.dv[row * 128 + d - 192] = __float2bfloat16_rn(sum);
+    const int unit = blockIdx.x * 4 + threadIdx.x / 80, d = threadIdx.x % 80 * 4;
+    const int group = unit % p.hkv, row = unit / p.hkv;
+    if (row >= p.row0[p.n_seqs]) return;
+    int q = 0;  // its sequence: the last one that starts at or before the row
+    for (int n = p.n_seqs; n > 1;) {
+        const int half = n / 2;
+        if (p.row0[q + half] <= row) {
+            q += half;
+            n -= half;
+        } else {
+            n = half;
+        }
+    }
+    const int u = row - p.row0[q], L = p.len[q];
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto add = [&](const float *src, size_t step, int n) {
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(src + i * step));
+            sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+        }
+    };
+    if (p.split.chunks > 1) {
+        const int tile = u / kBwdKeyTile;
+        const size_t slot = static_cast<size_t>(p.tile_slot[q] + tile * p.split.chunks) * p.hkv + group;
+        add(p.tile_part + (slot * kBwdKeyTile + u % kBwdKeyTile) * 320 + d, static_cast<size_t>(p.hkv) * kBwdKeyTile * 320,
+            (bwd_tile_steps(L, tile * kBwdKeyTile, p.window) + p.split.chunk_steps - 1) / p.split.chunk_steps);
+    }
+    if (u < p.sinks && p.slot[q] >= 0) {
+        const int first = p.split.chunks > 1 ? 1 : 0;
+        const size_t slot = static_cast<size_t>(p.slot[q] + first) * p.hkv + group;
+        add(p.part + (slot * p.sinks + u) * 320 + d, static_cast<size_t>(p.hkv) * p.sinks * 320,
+            bwd_sink_chunks(L, p.window, p.split.sink_steps) + 1 - first);
+    }
+    const size_t out = static_cast<size_t>(p.start[q] + u) * p.hkv + group;
+    __nv_bfloat16 *dst = d < 192 ? p.dk + out * 192 + d : p.dv + out * 128 + d - 192;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
 }
 
 cudaError_t launch_bwd_sink_sum(const BwdSinkSum &sum, cudaStream_t stream) {
-    const unsigned grid = static_cast<unsigned>(sum.n_seqs) * sum.hkv * sum.sinks;
-    gdla_bwd_sink_sum_kernel<<<grid, 320, 0, stream>>>(sum);
+    const unsigned units = static_cast<unsigned>(sum.row0[sum.n_seqs]) * sum.hkv;
+    gdla_bwd_sink_sum_kernel<<<(units + 3) / 4, 320, 0, stream>>>(sum);
     return cudaPeekAtLastError();
 }
 
@@ -898,7 +936,8 @@ static cudaError_t launch_dkv_sized(const BwdLaunch &L, const Plan &plan, cudaSt
     const long long work = static_cast<long long>(plan.n_items) * plan.hkv;
     const unsigned grid = static_cast<unsigned>(work < num_sms ? work : num_sms);
     gdla_bwd_dkv_kernel<Plan, SINK><<<grid, pbk::NUM_THREADS, pbk::SMEM_BYTES, stream>>>(
-        L.tm_qs12, L.tm_qn12, L.tm_dhs12, L.tm_dhn12, L.tm_k128, L.tm_v128, L.tm_stats, L.dk, L.dv, L.part, plan);
+        L.tm_qs12, L.tm_qn12, L.tm_dhs12, L.tm_dhn12, L.tm_k128, L.tm_v128, L.tm_stats, L.dk, L.dv, L.part, L.tile_part,
+        plan);
     return cudaPeekAtLastError();
 }
 
@@ -914,7 +953,9 @@ static cudaError_t with_sized_plan(const PrefillPlan &plan, F &&launch) {
         small.n_seqs = plan.n_seqs;
         std::memcpy(small.seq_start, plan.seq_start, sizeof(int) * plan.n_seqs);
         std::memcpy(small.seq_len, plan.seq_len, sizeof(int) * plan.n_seqs);
+        small.split = plan.split;
         std::memcpy(small.part, plan.part, sizeof(int) * plan.n_seqs);
+        std::memcpy(small.tile_part, plan.tile_part, sizeof(int) * plan.n_seqs);
         std::memcpy(small.items, plan.items, sizeof(uint32_t) * plan.n_items);
     };
     if (plan.n_items <= PrefillPlanSmall::kMaxItems && plan.n_seqs <= PrefillPlanSmall::kMaxSeqs) {

@@ -79,7 +79,10 @@ def _plain_grads(t, dout, seqlens, window, sinks):
     return dict(zip(GRADS, g))
 
 
-@pytest.mark.parametrize("seqlens, heads, window, sinks", SHAPES + [((2500, 100, 1400), 1, 64, 5), ((3001,), 2, 128, 100)])
+@pytest.mark.parametrize("seqlens, heads, window, sinks", SHAPES + [
+    ((2500, 100, 1400), 1, 64, 5), ((3001,), 2, 128, 100),      # key tiles in 2 parts and more, and later chunks
+    ((1, 129, 257, 90, 1000), 1, 1000, 3), ((5000,), 1, 40, 128),
+    ((300,) * 60, 1, 100, 4)])                                  # enough tiles: not cut
 def test_backward(seqlens, heads, window, sinks):
     t = gi.make_prefill_inputs(seqlens, heads, 7 + window, device="cuda")
     dout = gi.make_prefill_grad(seqlens, heads, 7 + window, device="cuda")

@@ -120,7 +120,8 @@ def test_sinks_workspace(lib):
     base = gdla.attn_bwd_workspace_bytes
     assert size((4096,), 16, 0, 4) == base(4096, 16)          # no window: no sinks
     assert size((4096,), 16, 5000, 4) == base(4096, 16)       # a window over everything
-    assert size((200, 100), 2, 128, 4) == base(300, 2)        # every row within the first key tile's reach
+    assert size((200, 100) * 40, 2, 128, 4) == base(12000, 2)  # every row within the first key tile's reach
+    assert size((200, 100), 2, 128, 4) > base(300, 2)          # few key tiles: cut, so with partials
     assert size((4096,), 16, 128, 4) > base(4096, 16)
     assert size((4096,), 16, 128, 8) > size((4096,), 16, 128, 4)
     assert size((4096,), 65, 128, 4) == 0
