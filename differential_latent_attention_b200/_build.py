@@ -1,21 +1,26 @@
-"""Builds libgdla.so (sm_100a) in-tree with nvcc.
+"""Builds libgdla.so (sm_100a) and the binding of its paged-cache calls in-tree, with nvcc and g++.
 
 The library is one translation unit (csrc/gdla_lib.cu). cudart is linked
 statically and the driver API is reached through cudaGetDriverEntryPoint, so
 the .so loads on machines without a GPU driver (its calls then fail with
-GDLA_ERR_CUDA).
+GDLA_ERR_CUDA). The binding (csrc/gdla_binding.cpp, a CPython extension on
+PyTorch's headers) takes the library's functions by address and links against
+PyTorch alone.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libgdla.so")
+BINDING_PATH = os.path.join(PKG, "_gdla_binding.so")
+BINDING_SOURCES = [os.path.join(CSRC, "gdla_binding.cpp"), os.path.join(INCLUDE, "gdla.h")]
 SOURCES = ["gdla_lib.cu", "gdla_api.cu", "gdla_prefill.cu", "gdla_prefill_bwd.cu", "gdla_prologue.cu", "gdla_decode.cu", "gdla_decode_noalloc.cu",
            "gdla_decode_latent.cu", "gdla_selftest.cu", "gdla_internal.h", "gdla_ptx.cuh", "gdla_prologue.h",
            "gdla_pair.cuh", "gdla_paged.cuh", "gdla_cache_append.cu", "gdla_decode_paged.cu"]
@@ -42,8 +47,36 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def _compile(cmd):
+    # the compiler's intermediate files stay inside the repository
+    scratch = os.path.join(os.path.dirname(PKG), "_build", "tmp")
+    os.makedirs(scratch, exist_ok=True)
+    subprocess.check_call(cmd, env={**os.environ, "TMPDIR": scratch})
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/gdla_binding.cpp into _gdla_binding.so next to this file."""
+    if not force and os.path.exists(BINDING_PATH):
+        t = os.path.getmtime(BINDING_PATH)
+        if all(os.path.getmtime(f) <= t for f in [*BINDING_SOURCES, __file__]):
+            return BINDING_PATH
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    _compile(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+              "-isystem", os.path.join(base, "include"), "-isystem", os.path.join(base, "include/torch/csrc/api/include"),
+              "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+              "-o", tmp, BINDING_SOURCES[0], "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+              "-ltorch", "-ltorch_python"])
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/gdla_lib.cu into libgdla.so next to this file."""
+    """Compile csrc/gdla_lib.cu into libgdla.so next to this file, and the binding beside it."""
+    build_binding(force)
     if not force and up_to_date():
         return LIB_PATH
     tmp = LIB_PATH + f".tmp{os.getpid()}"
@@ -52,10 +85,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
            os.path.join(CSRC, "gdla_lib.cu")]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
-    # the compiler's intermediate files stay inside the repository
-    scratch = os.path.join(os.path.dirname(PKG), "_build", "tmp")
-    os.makedirs(scratch, exist_ok=True)
-    subprocess.check_call(cmd, env={**os.environ, "TMPDIR": scratch})
+    _compile(cmd)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

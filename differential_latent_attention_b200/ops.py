@@ -1,4 +1,5 @@
-"""ctypes binding of libgdla.so: argument marshalling only.
+"""Binding of libgdla.so: argument marshalling only, by ctypes and, for the paged-cache calls,
+by a CPython extension (csrc/gdla_binding.cpp).
 
 Every step of the GDLA core runs in the library's CUDA kernels; PyTorch only
 provides device memory and the current CUDA stream. There is no fallback: if
@@ -7,6 +8,7 @@ libgdla.so is missing or cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -31,8 +33,6 @@ DL = DC + DR
 LATENT_MAX_KV_HEADS = 16
 MAX_SINKS = 128
 PAGE_SIZES = (16, 32, 64, 128)
-CACHE_BF16, CACHE_E4M3 = 0, 1
-ERR_WORKSPACE = 3
 SELFTEST_SITE = 0x30001  # GDLA_SELFTEST_SITE
 
 _lib = None
@@ -89,7 +89,8 @@ def library():
             lib.gdla_cache_append.argtypes = [p, ll, ll, p, ll, p, ll, ll, p, p, p, p, i, i, i, p, i, p, i, p, i, i, i,
                                               p]
             lib.gdla_cache_append.restype = i
-            lib.gdla_attn_decode_paged.argtypes = [p, p, p, p, p, p, i, i, i, p, i, p, i, p, p, p, i, i, i, i, i, p, sz, p]
+            lib.gdla_attn_decode_paged.argtypes = [p, p, p, p, p, p, i, i, i, p, i, p, i, p, p, p, i, i, i, i, i, p, sz,
+                                                   p]
             lib.gdla_attn_decode_paged.restype = i
             lib.gdla_decode_paged_workspace_bytes.argtypes = [i, i, i, i, i]
             lib.gdla_decode_paged_workspace_bytes.restype = sz
@@ -186,7 +187,7 @@ def attn_fwd(q_sig, q_noise, k, v, lam, gate, seqlens, window=0, out=None, strea
     _check(lam, "lam", torch.float32, (n, hs))
     _check(gate, "gate", torch.bfloat16, (n, hs, DV))
     if out is None:
-        out = torch.empty((n, hs, DV), dtype=torch.bfloat16, device=q_sig.device)
+        out = torch.empty_like(gate)
     _check(out, "out", torch.bfloat16, (n, hs, DV))
     _on_one_device(stream, (("q_sig", q_sig), ("q_noise", q_noise), ("k", k), ("v", v), ("lam", lam),
                             ("gate", gate), ("out", out)))
@@ -235,7 +236,7 @@ def attn_bwd(q_sig, q_noise, k, v, lam, gate, dout, seqlens, window=0, grads=Non
               "dk": ((n, hkv, DQK), torch.bfloat16), "dv": ((n, hkv, DV), torch.bfloat16),
               "dlambda": ((n, hs), torch.float32), "dgate": ((n, hs, DV), torch.bfloat16)}
     if grads is None:
-        grads = {name: torch.empty(shape, dtype=dt, device=q_sig.device) for name, (shape, dt) in shapes.items()}
+        grads = {name: torch.empty_like(t) for name, t in zip(shapes, (q_sig, q_noise, k, v, lam, gate))}
     for name, (shape, dt) in shapes.items():
         _check(grads[name], name, dt, shape)
     need = attn_bwd_sinks_workspace_bytes(lens, hkv, window, sinks) if sinks else attn_bwd_workspace_bytes(n, hkv)
@@ -397,74 +398,26 @@ def attn_decode_latent(q_abs_sig, q_abs_noise, ckv, cu_seqlens_k, max_seqlen_k, 
     return out
 
 
-# The paged-cache calls are made once per layer and token, so their checks are one
-# combined test per tensor, which hands back the pointer; what failed is worked out only then.
-def _dense(t, name, dtype, shape, dev):
-    """The pointer of a contiguous tensor of this type and shape on CUDA device ``dev``."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == dev
-            and t.is_contiguous()):
-        return t.data_ptr()
-    _check(t, name, dtype, shape)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, k_pages on cuda:{dev}")
-    return t.data_ptr()
+_native = None
 
 
-def _cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, stream):
-    """The paged cache's own arguments and the launch stream, checked: (device, sizes, pointers)."""
-    if not isinstance(k_pages, torch.Tensor) or not isinstance(block_table, torch.Tensor):
-        raise TypeError("k_pages and block_table must be torch.Tensors")
-    if k_pages.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("expected k_pages [pages, H, page_size, 192] and block_table [batch, pages per sequence]")
-    dev = k_pages.get_device()
-    if dev < 0:
-        raise ValueError("k_pages must be on a CUDA device")
-    np_, hkv, ps, _ = k_pages.shape
-    b, width = block_table.shape
-    dt = k_pages.dtype
-    ks = vs = 0
-    if dt is torch.bfloat16:
-        kind = CACHE_BF16
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("k_scale and v_scale belong to an e4m3 cache")
-    elif dt is torch.float8_e4m3fn:
-        kind = CACHE_E4M3
-        ks = _dense(k_scale, "k_scale", torch.float32, (np_, hkv), dev)
-        vs = _dense(v_scale, "v_scale", torch.float32, (np_, hkv), dev)
-    else:
-        raise TypeError(f"k_pages: expected torch.bfloat16 or torch.float8_e4m3fn, got {dt}")
-    kp = _dense(k_pages, "k_pages", dt, (np_, hkv, ps, DQK), dev)
-    vp = _dense(v_pages, "v_pages", dt, (np_, hkv, ps, DV), dev)
-    bt = _dense(block_table, "block_table", torch.int32, (b, width), dev)
-    sl = _dense(seqlens_k, "seqlens_k", torch.int32, (b,), dev)
-    sdev = torch.cuda.current_device() if stream is None else stream.device.index
-    if sdev != dev:
-        raise ValueError(f"the tensors are on cuda:{dev} but the launch stream is on cuda:{sdev}")
-    return dev, kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl
-
-
-def _rows(t, name, shape, dev):
-    """(pointer, strides of all but the last dimension) of a bf16 CUDA tensor whose last dimension is dense; the
-    others may be views."""
-    if not (type(t) is torch.Tensor and t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype is not torch.bfloat16:
-            raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be on a CUDA device")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, k_pages on cuda:{dev}")
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name}: its last dimension must be contiguous")
-    if shape[0] == 1 or shape[-2] == 1:
-        st = [0 if size == 1 else x for size, x in zip(shape, st)]   # one row: its stride says nothing
-    if (st[0] | st[-2]) & 7:
-        raise ValueError(f"{name}: strides must be multiples of 8 elements, got {t.stride()}")
-    return t.data_ptr(), st[0], st[-2]
+def _paged():
+    """The extension that checks and makes the paged-cache calls, given the loaded library's functions."""
+    global _native
+    mod = _native
+    if mod is None:
+        lib = library()
+        path = _build.BINDING_PATH
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing; build it with `python -m "
+                               f"differential_latent_attention_b200._build` (no fallback path exists)")
+        spec = importlib.util.spec_from_file_location("_gdla_binding", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+            lib.gdla_cache_append, lib.gdla_attn_decode_paged, lib.gdla_decode_paged_workspace_bytes)))
+        _native = mod
+    return mod
 
 
 def cache_append(k_nope, k_rope, v, k_pages, v_pages, block_table, cu_seqlens_new, seqlens_k, k_scale=None,
@@ -481,15 +434,8 @@ def cache_append(k_nope, k_rope, v, k_pages, v_pages, block_table, cu_seqlens_ne
     b, which then holds seqlens_k[b] tokens. ``rotate`` turns k_rope to each token's
     position on the way. Pages and scales are updated in place.
     """
-    dev, kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl = _cache(k_pages, v_pages, k_scale, v_scale, block_table,
-                                                                       seqlens_k, stream)
-    n = v.shape[0] if isinstance(v, torch.Tensor) and v.dim() else -1
-    kn, kn_t, kn_h = _rows(k_nope, "k_nope", (n, hkv, DQK - DR), dev)
-    kr, kr_t, _ = _rows(k_rope, "k_rope", (n, DR), dev)
-    vv, v_t, v_h = _rows(v, "v", (n, hkv, DV), dev)
-    cu = _dense(cu_seqlens_new, "cu_seqlens_new", torch.int32, (b + 1,), dev)
-    st = library().gdla_cache_append(kn, kn_t, kn_h, kr, kr_t, vv, v_t, v_h, kp, vp, ks, vs, kind, np_, ps, bt, width,
-                                     cu, n, sl, b, hkv, 1 if rotate else 0, _stream(stream))
+    st = _paged().cache_append(k_nope, k_rope, v, k_pages, v_pages, block_table, cu_seqlens_new, seqlens_k, k_scale,
+                               v_scale, rotate, stream)
     if st != 0:
         raise GDLAError(st, "gdla_cache_append")
 
@@ -510,33 +456,11 @@ def attn_decode_paged(q_sig, q_noise, k_pages, v_pages, block_table, seqlens_k, 
     position first. ``workspace`` (uint8 CUDA tensor) is allocated here when not given.
     Returns out [B, 4H, 128] bf16.
     """
-    dev, kind, np_, hkv, ps, b, width, kp, vp, ks, vs, bt, sl = _cache(k_pages, v_pages, k_scale, v_scale, block_table,
-                                                                       seqlens_k, stream)
-    hs = GROUP * hkv
-    qs = _dense(q_sig, "q_sig", torch.bfloat16, (b, hs, DQK), dev)
-    qn = _dense(q_noise, "q_noise", torch.bfloat16, (b, hkv, DQK), dev)
-    lm = _dense(lam, "lam", torch.float32, (b, hs), dev)
-    gt = _dense(gate, "gate", torch.bfloat16, (b, hs, DV), dev)
-    if out is None:
-        out = torch.empty_like(gate)
-    ot = _dense(out, "out", torch.bfloat16, (b, hs, DV), dev)
-    fn = library().gdla_attn_decode_paged
-    args = (qs, qn, kp, vp, ks, vs, kind, np_, ps, bt, width, sl, int(max_seqlen_k), lm, gt, ot, b, hkv, int(window),
-            int(sinks), 1 if rotate else 0)
-    if workspace is None:
-        st = fn(*args, 0, 0, _stream(stream))
-        if st == ERR_WORKSPACE:  # the few sizes that need one
-            workspace = _scratch(decode_paged_workspace_bytes(b, hkv, max_seqlen_k, window, sinks), q_sig.device,
-                                 stream)
-            st = fn(*args, workspace.data_ptr(), workspace.numel(), _stream(stream))
-    else:
-        _check_workspace(workspace)
-        if workspace.get_device() != dev:
-            raise ValueError(f"workspace is on cuda:{workspace.get_device()}, k_pages on cuda:{dev}")
-        st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
-    if st != 0:
-        raise GDLAError(st, "gdla_attn_decode_paged")
-    return out
+    got = _paged().attn_decode_paged(q_sig, q_noise, k_pages, v_pages, block_table, seqlens_k, max_seqlen_k, lam, gate,
+                                     window, sinks, k_scale, v_scale, rotate, out, workspace, stream)
+    if type(got) is int:
+        raise GDLAError(got, "gdla_attn_decode_paged")
+    return got
 
 
 def device_error(clear=True) -> int:

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import differential_latent_attention_b200 as gdla
-from differential_latent_attention_b200 import _build, ops
+from differential_latent_attention_b200 import _build
 
 FAKE = 0x10000
 
@@ -133,72 +133,93 @@ def test_sinks_workspace(lib):
     assert _sinks(lib, [4096], True, heads=2, ws=FAKE + 16) == 3
 
 
-def _cpu_cache(dtype=torch.bfloat16):
-    return dict(k_pages=torch.zeros((2, 1, 16, 192), dtype=dtype), v_pages=torch.zeros((2, 1, 16, 128), dtype=dtype),
-                block_table=torch.zeros((1, 2), dtype=torch.int32), seqlens_k=torch.ones(1, dtype=torch.int32))
+# The binding looks at the device last, so on host tensors every other check can be seen; a call that passes them all
+# ends with the refusal of host tensors.
+def _cache(dtype=torch.bfloat16, pages=2, heads=3, page=16, batch=2, width=2):
+    c = dict(k_pages=torch.zeros((pages, heads, page, 192), dtype=dtype), v_pages=torch.zeros((pages, heads, page, 128), dtype=dtype),
+             block_table=torch.zeros((batch, width), dtype=torch.int32), seqlens_k=torch.ones(batch, dtype=torch.int32))
+    if dtype == torch.float8_e4m3fn:
+        c.update(k_scale=torch.ones((pages, heads)), v_scale=torch.ones((pages, heads)))
+    return c
 
 
-def test_binding_refuses_host_tensors_and_wrong_caches():
-    c = _cpu_cache()
-    new = dict(k_nope=torch.zeros((1, 1, 128), dtype=torch.bfloat16), k_rope=torch.zeros((1, 64), dtype=torch.bfloat16),
-               v=torch.zeros((1, 1, 128), dtype=torch.bfloat16), cu_seqlens_new=torch.tensor([0, 1], dtype=torch.int32))
-    with pytest.raises(ValueError, match="CUDA"):
-        gdla.cache_append(**new, **c)
-    q = dict(q_sig=torch.zeros((1, 4, 192), dtype=torch.bfloat16), q_noise=torch.zeros((1, 1, 192), dtype=torch.bfloat16),
-             lam=torch.zeros(1, 4), gate=torch.zeros((1, 4, 128), dtype=torch.bfloat16), max_seqlen_k=16)
-    with pytest.raises(ValueError, match="CUDA"):
-        gdla.attn_decode_paged(**q, **c)
-    with pytest.raises(ValueError, match="expected k_pages"):
-        gdla.attn_decode_paged(**q, **{**c, "k_pages": c["k_pages"][0]})
-    with pytest.raises(TypeError):
-        gdla.attn_decode_paged(**q, **{**c, "k_pages": None})
+def _new(n=5, heads=3, batch=2):
+    bf = torch.bfloat16
+    return dict(k_nope=torch.zeros((n, heads, 128), dtype=bf), k_rope=torch.zeros((n, 64), dtype=bf),
+                v=torch.zeros((n, heads, 128), dtype=bf), cu_seqlens_new=torch.zeros(batch + 1, dtype=torch.int32))
 
 
-class _Fake(torch.Tensor):
-    """A tensor that says it is on cuda:0 (no launch is reached with it)."""
-
-    def get_device(self):
-        return 0
-
-    @property
-    def is_cuda(self):
-        return True
+def _query(batch=2, heads=3):
+    bf = torch.bfloat16
+    return dict(q_sig=torch.zeros((batch, 4 * heads, 192), dtype=bf), q_noise=torch.zeros((batch, heads, 192), dtype=bf),
+                lam=torch.zeros(batch, 4 * heads), gate=torch.zeros((batch, 4 * heads, 128), dtype=bf), max_seqlen_k=16)
 
 
-def _fake(t):
-    return t.as_subclass(_Fake)
+KINDS = [torch.bfloat16, torch.float8_e4m3fn]
 
 
-def test_row_views():
-    """What the appended rows may look like: dense last dimension, strides of whole 16-byte units."""
-    k = _fake(torch.zeros((5, 3, 192), dtype=torch.bfloat16))
-    nope, rope = k[..., :128], k[:, 0, 128:]
-    assert ops._rows(nope, "k_nope", (5, 3, 128), 0)[1:] == (576, 192)
-    assert ops._rows(rope, "k_rope", (5, 64), 0)[1:] == (576, 576)
-    shared = _fake(torch.zeros((5, 1, 128), dtype=torch.bfloat16)).expand(5, 3, 128)
-    assert ops._rows(shared, "v", (5, 3, 128), 0)[1:] == (128, 0)
-    one = _fake(torch.zeros((1, 1, 131), dtype=torch.bfloat16))[..., :128]   # a stride that is never used
-    assert ops._rows(one, "v", (1, 1, 128), 0)[1:] == (0, 0)
-    odd = _fake(torch.zeros((5, 3, 132), dtype=torch.bfloat16))[..., :128]
-    with pytest.raises(ValueError, match="multiples of 8"):
-        ops._rows(odd, "k_nope", (5, 3, 128), 0)
-    with pytest.raises(ValueError, match="contiguous"):
-        ops._rows(_fake(torch.zeros((5, 128, 3), dtype=torch.bfloat16)).transpose(1, 2), "v", (5, 3, 128), 0)
-    with pytest.raises(ValueError, match="shape"):
-        ops._rows(nope, "k_nope", (5, 2, 128), 0)
-    with pytest.raises(TypeError):
-        ops._rows(_fake(torch.zeros((5, 3, 128))), "v", (5, 3, 128), 0)
-    with pytest.raises(ValueError, match="cuda:0"):
-        ops._rows(nope, "k_nope", (5, 3, 128), 1)
+@pytest.mark.parametrize("dtype", KINDS)
+def test_binding_refuses_host_tensors_last(dtype):
+    with pytest.raises(ValueError, match="CUDA device"):
+        gdla.cache_append(**_new(), **_cache(dtype))
+    with pytest.raises(ValueError, match="CUDA device"):
+        gdla.attn_decode_paged(**_query(), **_cache(dtype), window=128, sinks=4, rotate=True)
 
 
-def test_e4m3_cache_wants_scales_and_bf16_none():
-    c = {k: _fake(v) for k, v in _cpu_cache(torch.float8_e4m3fn).items()}
-    with pytest.raises(TypeError, match="k_scale"):
-        ops._cache(c["k_pages"], c["v_pages"], None, None, c["block_table"], c["seqlens_k"], None)
-    b = {k: _fake(v) for k, v in _cpu_cache().items()}
-    s = _fake(torch.ones((2, 1)))
+@pytest.mark.parametrize("call, base", [(gdla.cache_append, _new), (gdla.attn_decode_paged, _query)])
+def test_binding_checks_the_cache(call, base):
+    good = {**base(), **_cache(torch.float8_e4m3fn)}
+    for name, value, error in (
+            ("k_pages", None, TypeError), ("block_table", 3, TypeError),
+            ("k_pages", good["k_pages"][0], ValueError), ("block_table", good["block_table"][0], ValueError),
+            ("k_pages", good["k_pages"].float(), TypeError),                     # neither cache type
+            ("k_pages", good["k_pages"][..., :128].contiguous(), ValueError),
+            ("v_pages", torch.zeros((2, 3, 16, 128), dtype=torch.bfloat16), TypeError),
+            ("v_pages", good["v_pages"][:1], ValueError),
+            ("v_pages", torch.zeros((2, 3, 128, 16), dtype=torch.float8_e4m3fn).transpose(2, 3), ValueError),
+            ("k_scale", None, TypeError), ("v_scale", None, TypeError), ("k_scale", torch.ones(2, 4), ValueError),
+            ("k_scale", torch.ones((2, 3), dtype=torch.float64), TypeError),
+            ("block_table", good["block_table"].long(), TypeError),
+            ("seqlens_k", good["seqlens_k"].long(), TypeError), ("seqlens_k", torch.ones(3, dtype=torch.int32), ValueError)):
+        with pytest.raises(error) as e:
+            call(**{**good, name: value})
+        assert "CUDA device" not in str(e.value), name
     with pytest.raises(ValueError, match="e4m3"):
-        ops._cache(b["k_pages"], b["v_pages"], s, s, b["block_table"], b["seqlens_k"], None)
-    with pytest.raises(TypeError, match="float8"):
-        ops._cache(_fake(torch.zeros((2, 1, 16, 192))), b["v_pages"], None, None, b["block_table"], b["seqlens_k"], None)
+        call(**{**base(), **_cache(), "k_scale": torch.ones((2, 3)), "v_scale": torch.ones((2, 3))})
+
+
+def test_append_checks_its_rows():
+    """Dense last dimension, strides of whole 16-byte units, one row's stride says nothing."""
+    wide = torch.zeros((5, 3, 192), dtype=torch.bfloat16)
+    shared = torch.zeros((5, 1, 128), dtype=torch.bfloat16).expand(5, 3, 128)
+    c = _cache()
+    for rows in (dict(k_nope=wide[..., :128], k_rope=wide[:, 0, 128:]), dict(v=shared)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            gdla.cache_append(**{**_new(), **rows}, **c)
+    one = torch.zeros((1, 1, 131), dtype=torch.bfloat16)[..., :128]
+    with pytest.raises(ValueError, match="CUDA device"):
+        gdla.cache_append(**{**_new(1, 1), "k_nope": one, "v": one}, **_cache(heads=1))
+    odd = torch.zeros((5, 3, 132), dtype=torch.bfloat16)[..., :128]
+    for rows, error, match in (
+            (dict(k_nope=odd), ValueError, "multiples of 8"), (dict(v=odd), ValueError, "multiples of 8"),
+            (dict(k_rope=torch.zeros((5, 68), dtype=torch.bfloat16)[:, :64]), ValueError, "multiples of 8"),
+            (dict(v=torch.zeros((5, 128, 3), dtype=torch.bfloat16).transpose(1, 2)), ValueError, "contiguous"),
+            (dict(k_nope=wide[:, :2, :128]), ValueError, "k_nope: expected shape"),
+            (dict(k_rope=torch.zeros((4, 64), dtype=torch.bfloat16)), ValueError, "k_rope: expected shape"),
+            (dict(v=torch.zeros((5, 3, 128))), TypeError, "v: expected BFloat16"),
+            (dict(v=None), TypeError, "v must be"),
+            (dict(cu_seqlens_new=torch.zeros(2, dtype=torch.int32)), ValueError, "cu_seqlens_new")):
+        with pytest.raises(error, match=match):
+            gdla.cache_append(**{**_new(), **rows}, **c)
+
+
+def test_decode_checks_its_queries():
+    c, q = _cache(), _query()
+    for name, value, error in (
+            ("q_sig", q["q_sig"][:, :11], ValueError), ("q_noise", q["q_noise"].float(), TypeError),
+            ("q_sig", torch.zeros((2, 192, 12), dtype=torch.bfloat16).transpose(1, 2), ValueError),
+            ("lam", q["lam"].double(), TypeError), ("gate", q["gate"][..., :64], ValueError),
+            ("max_seqlen_k", "long", TypeError), ("max_seqlen_k", 2 ** 40, ValueError), ("window", 1.5, TypeError)):
+        with pytest.raises(error) as e:
+            gdla.attn_decode_paged(**{**q, name: value}, **c)
+        assert "CUDA device" not in str(e.value), name
