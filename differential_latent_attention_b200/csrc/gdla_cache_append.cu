@@ -27,39 +27,52 @@ namespace gdla {
 // cu[b] / P + 2 b .. cu[b + 1] / P + 2 (b + 1) - 1, which is room for the
 // floor(n / P) + 2 pages that n tokens can touch; the units that it leaves over do nothing.
 struct AppendUnit {
-    bool live;
+    bool fits;           // the unit has tokens (its page is still to be checked)
     int page;            // page of the pool
     int pos0;            // position of slot 0
     int slot0, slot1;    // slots that the call fills
     int tok0;            // token of slot0
 };
-// The whole warp calls. The sequence is the last one whose first unit is <= u: each round the
-// lanes try 32 places of what is left, so 1,024 sequences take two dependent loads.
-__device__ __forceinline__ AppendUnit append_unit(const AppendPlan &p, int u) {
-    AppendUnit a{};
+// The sequence of unit u, the last one whose first unit is <= u; the whole warp calls. A step's
+// sequences bring about one token each, so STEP looks first where u would be if all did. Otherwise each round the
+// lanes try 32 places of what is left: 1,024 sequences take two dependent loads.
+template <bool STEP>
+__device__ __forceinline__ int append_sequence(const AppendPlan &p, int u) {
+    const auto first = [&](int b) { return (p.cu_new[b] >> p.page_shift) + 2 * b; };
+    if (STEP) {
+        const int b = min(static_cast<int>((static_cast<long long>(u) << p.page_shift) / (2 * p.page_size + 1)), p.batch - 1);
+        if (first(b) <= u && u < first(b + 1)) return b;
+    }
     const int lane = threadIdx.x & 31;
     int b = 0, left = p.batch;  // it is one of b .. b + left - 1
     while (left > 1) {
         const int step = (left + 31) / 32, mine = b + lane * step;
-        const bool before = lane * step < left && (p.cu_new[mine] >> p.page_shift) + 2 * mine <= u;
+        const bool before = lane * step < left && first(mine) <= u;
         const int hits = __popc(__ballot_sync(0xffffffffu, before));
         const int skip = max(hits - 1, 0) * step;
         b += skip;
         left = min(step, left - skip);
     }
+    return b;
+}
+template <bool STEP>
+__device__ __forceinline__ AppendUnit append_unit(const AppendPlan &p, int u) {
+    AppendUnit a{};
+    const int b = append_sequence<STEP>(p, u);
     const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1], len = p.seqlens_k[b];
     const int n = c1 - c0, before = len - n, P = p.page_size;
     if (c0 < 0 || n < 1 || c1 > p.num_tokens || before < 0 || len > p.max_pages * static_cast<long long>(P)) return a;
     const int first = (c0 >> p.page_shift) + 2 * b, j = (before >> p.page_shift) + (u - first);
     if (u < first || j > (len - 1) >> p.page_shift) return a;
+    a.fits = true;
     a.page = p.block_table[static_cast<size_t>(b) * p.max_pages + j];
-    a.live = a.page >= 0 && a.page < p.num_pages;
     a.pos0 = j << p.page_shift;
     a.slot0 = max(before, a.pos0) - a.pos0;
     a.slot1 = min(len - a.pos0, P);
     a.tok0 = c0 + a.pos0 + a.slot0 - before;
     return a;
 }
+__device__ __forceinline__ bool in_pool(const AppendPlan &p, int page) { return page >= 0 && page < p.num_pages; }
 
 // Largest |x| of eight bf16 as fp32 bits: integers order like the numbers, and what is not
 // finite is 0x7F800000 or more.
@@ -174,8 +187,8 @@ gdla_cache_append_kernel(const __grid_constant__ AppendPlan p) {
     __shared__ uint32_t red[2][2][8];
     const int groups = (p.hkv + p.heads_per_cta - 1) / p.heads_per_cta;
     const int u = blockIdx.x / groups;
-    const AppendUnit a = append_unit(p, u);
-    if (!a.live) return;
+    const AppendUnit a = append_unit<false>(p, u);
+    if (!a.fits) return;
     const int n = a.slot1 - a.slot0, t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int row = t >> 4, col = t & 15;     // pieces (row + 16 i, col)
     const int rrow = t >> 2, rq = t & 3;      // rotary pieces (rrow + 64 i, rq)
@@ -189,6 +202,7 @@ gdla_cache_append_kernel(const __grid_constant__ AppendPlan p) {
             if (E4M3) rope_max = max(rope_max, max(max_bits(rope[i].lo, false), max_bits(rope[i].hi, false)));
         }
     }
+    if (!in_pool(p, a.page)) return;
     const int h0 = (blockIdx.x - u * groups) * p.heads_per_cta, h1 = min(p.hkv, h0 + p.heads_per_cta);
     const size_t tok = static_cast<size_t>(a.tok0 + row);
     const __nv_bfloat16 *k_src = p.k_nope + tok * p.nope_token + h0 * p.nope_head + 8 * col;
@@ -296,8 +310,8 @@ gdla_cache_append_step_kernel(const __grid_constant__ AppendPlan p, int units) {
     const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int u = w / p.hkv, h = w - u * p.hkv;
     if (u >= units) return;
-    const AppendUnit a = append_unit(p, u);
-    if (!a.live) return;
+    const AppendUnit a = append_unit<true>(p, u);
+    if (!a.fits) return;
     const int n = a.slot1 - a.slot0;
     const bool is_k = lane < 16;
     const __nv_bfloat16 *src = is_k ? p.k_nope + static_cast<size_t>(a.tok0) * p.nope_token + h * p.nope_head + 8 * lane
@@ -305,15 +319,20 @@ gdla_cache_append_step_kernel(const __grid_constant__ AppendPlan p, int units) {
     const long long step = is_k ? p.nope_token : p.v_token;
     const auto piece = [&](int r) { return __ldg(reinterpret_cast<const uint4 *>(src + r * step)); };
     const auto turned = [&](int r) { return rope_part(p, a.tok0 + r, a.pos0 + a.slot0 + r, lane & 3); };
+    // the last row (of a step: the only one) is under way while the page's entry comes
+    uint4 x0 = piece(n - 1);
+    RopePart q0;
+    if (lane < 4) q0 = turned(n - 1);
+    if (!in_pool(p, a.page)) return;
     const size_t blk = static_cast<size_t>(a.page) * p.hkv + h, slot = (blk << p.page_shift) + a.slot0;
     if constexpr (!E4M3) {
         __nv_bfloat16 *kd = static_cast<__nv_bfloat16 *>(p.k_pages) + slot * 192;
         __nv_bfloat16 *vd = static_cast<__nv_bfloat16 *>(p.v_pages) + slot * 128;
-        for (int r = 0; r < n; ++r) {
-            const uint4 x = piece(r);
+        for (int r = n - 1; r >= 0; --r) {
+            const uint4 x = r < n - 1 ? piece(r) : x0;
             *reinterpret_cast<uint4 *>(is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16)) = x;
             if (lane < 4) {
-                const RopePart q = turned(r);
+                const RopePart q = r < n - 1 ? turned(r) : q0;
                 *reinterpret_cast<uint4 *>(kd + r * 192 + 128 + 8 * lane) = to_bf16(q.lo);
                 *reinterpret_cast<uint4 *>(kd + r * 192 + 160 + 8 * lane) = to_bf16(q.hi);
             }
@@ -322,15 +341,13 @@ gdla_cache_append_step_kernel(const __grid_constant__ AppendPlan p, int units) {
         const bool goes_on = a.slot0 > 0;
         const float k_had = goes_on ? p.k_scale[blk] : 0.f, v_had = goes_on ? p.v_scale[blk] : 0.f;
         uint32_t km = 0u, vm = 0u;
-        uint4 x0 = make_uint4(0u, 0u, 0u, 0u);
-        RopePart q0;
         for (int r = 0; r < n; ++r) {  // the last row stays for the writing: with one row nothing is read twice
-            x0 = piece(r);
+            if (n > 1) x0 = piece(r);
             const uint32_t raw = max_bits(x0);
             const uint32_t m = raw < kInfBits ? raw : finite_max_bits(x0);
             if (is_k) km = max(km, m); else vm = max(vm, m);
             if (lane < 4) {
-                q0 = turned(r);
+                if (n > 1) q0 = turned(r);
                 km = max(km, max(max_bits(q0.lo, true), max_bits(q0.hi, true)));
             }
         }

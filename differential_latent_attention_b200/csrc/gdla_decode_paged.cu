@@ -33,6 +33,14 @@ namespace dp {
 constexpr int DQK = 192, DV = 128, HEADS = 5;
 constexpr int BLOCK = 16;       // keys per block
 constexpr int MAX_CLUSTER = 8;  // CTAs that join one (sequence, KV head) over distributed shared memory
+// A warp's O leaves its registers as [head][place], place 16 mt + 2 g8 + e for row g8 + 8 e of tile mt (rows of 132: the
+// sixteen lanes of a 64-bit store then take different banks). Sums keep that order; dim_of undoes it at the output.
+constexpr int RED_ROW = DV + 4;
+template <bool E4M3>
+__device__ __forceinline__ int dim_of(int place) {
+    const int mt = place >> 4, g8 = (place >> 1) & 7, e = place & 1;
+    return E4M3 ? 16 * g8 + 2 * mt + e : 16 * mt + g8 + 8 * e;
+}
 constexpr float kTrail = 4.f;  // a probability is at most 2^4; with a V scale's ratio of 2^8 it stays in f16
 constexpr float kScoreLog2 = 0.07216878364870322f * 1.4426950408889634f;  // log2(e) / sqrt(192)
 
@@ -45,8 +53,8 @@ struct Cfg {
     // blocks ahead: 10 KB in flight per warp either way, 16 warps per SM
     static constexpr int STAGES = E4M3 ? 2 : 1;
     static constexpr int RING = WARPS * STAGES * STAGE;
-    static constexpr int RED = WARPS * HEADS * DV * 4;  // fp32 [WARPS][5][128], over the ring once it is done
-    static constexpr int OFF_CTA = RING > RED ? RING : RED;        // fp32 [5][128]: this CTA's sums, then the heads
+    static constexpr int RED = WARPS * HEADS * RED_ROW * 4;  // fp32 [WARPS][5][132], over the ring once it is done
+    static constexpr int OFF_CTA = RING > RED ? RING : RED;        // fp32 [5][128]: this CTA's sums
     static constexpr int OFF_ML = OFF_CTA + HEADS * DV * 4;        // fp32 [WARPS][8][2], then [5][2] of the CTA
     static constexpr int OFF_AUX = OFF_ML + (WARPS + 1) * 64;      // float4 per stage: position, page, scales
     static constexpr int SMEM_BYTES = OFF_AUX + WARPS * STAGES * 16;
@@ -259,9 +267,7 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
                 look_up(n + 32, at_next, ks_next, vs_next);
             }
             const int at = __shfl_sync(0xffffffffu, at_cur, n & 31);
-            const float ks = __shfl_sync(0xffffffffu, ks_cur, n & 31), vs = __shfl_sync(0xffffffffu, vs_cur, n & 31);
             const int st = n % STAGES, pos0 = position(n);
-            if (lane == 0) aux[st] = make_float4(__int_as_float(pos0), __int_as_float(at), ks, vs);
             if (at >= 0) {
                 const size_t row = (static_cast<size_t>(at) << p.page_shift) + (pos0 & (p.page_size - 1));
                 const uint8_t *src = static_cast<const uint8_t *>(p.k_pages) + row * (DQK * C::ELT) + lane * 16;
@@ -287,6 +293,9 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
                     cp_async16(dst + v_place<E4M3>(unit / (8 * C::ELT), unit % (8 * C::ELT)), src + 512 * i);
                 }
             }
+            // the scales, whose loads the copies need not wait for
+            const float ks = __shfl_sync(0xffffffffu, ks_cur, n & 31), vs = __shfl_sync(0xffffffffu, vs_cur, n & 31);
+            if (lane == 0) aux[st] = make_float4(__int_as_float(pos0), __int_as_float(at), ks, vs);
         }
         cp_async_commit();
     };
@@ -471,7 +480,26 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
     }
     cp_async_wait<0>();
 
-    // the warps' sums over the ring
+    // What this thread will need of gate and lambda, under way while the sums are joined: outputs (signal head,
+    // place) i = thread, thread + THREADS, ..
+    const int n_part = p.splits / p.cluster;
+    const int share = DV / p.cluster, first = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) * share : 0;
+    constexpr int MAX_OUT = 4 * DV / C::THREADS;
+    __nv_bfloat16 gate_in[MAX_OUT];
+    float lam_in[MAX_OUT];
+    if (n_part == 1) {
+#pragma unroll
+        for (int j = 0; j < MAX_OUT; ++j) {
+            const int i = threadIdx.x + j * C::THREADS;
+            if (i < 4 * share) {
+                const size_t row = bg * 4 + i / share;
+                gate_in[j] = p.gate[row * DV + dim_of<E4M3>(first + i % share)];
+                lam_in[j] = __ldg(p.lambda + row);
+            }
+        }
+    }
+
+    // the warps' sums, each brought to the heads' maxima over the warps, over the ring
     float *red = reinterpret_cast<float *>(smem), *ml = reinterpret_cast<float *>(smem + C::OFF_ML);
     float *cta = reinterpret_cast<float *>(smem + C::OFF_CTA), *cml = ml + WARPS * 16;
 #pragma unroll
@@ -480,50 +508,47 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
         l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
     if (g8 == 0) *reinterpret_cast<float4 *>(ml + (warp * 8 + 2 * c) * 2) = make_float4(m0, l0, m1, l1);
-    if constexpr (E4M3) {
-#pragma unroll
-        for (int mt = 0; mt < DV / 16; ++mt) o[mt][0] *= vs_unit, o[mt][1] *= vs_unit, o[mt][2] *= vs_unit, o[mt][3] *= vs_unit;
-    }
     __syncthreads();
-    // rows g8 and g8 + 8 of tile mt: dims 16 g8 + 2 mt, + 1 (e4m3) or 16 mt + g8, + 8 (bf16)
-    const auto put = [&](int h, int mt, float x, float y) {
-        float *dst = red + (warp * HEADS + h) * DV;
-        if constexpr (E4M3) {
-            *reinterpret_cast<float2 *>(dst + 16 * g8 + 2 * mt) = make_float2(x, y);
-        } else {
-            dst[16 * mt + g8] = x;
-            dst[16 * mt + g8 + 8] = y;
-        }
-    };
+    float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        M0 = fmaxf(M0, ml[(w * 8 + 2 * c) * 2]);
+        M1 = fmaxf(M1, ml[(w * 8 + 2 * c + 1) * 2]);
+    }
+    float w0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M0), w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M1);
+    if constexpr (E4M3) w0 *= vs_unit, w1 *= vs_unit;
 #pragma unroll
     for (int mt = 0; mt < DV / 16; ++mt) {
-        if (2 * c < HEADS) put(2 * c, mt, o[mt][0], o[mt][2]);
-        if (2 * c + 1 < HEADS) put(2 * c + 1, mt, o[mt][1], o[mt][3]);
+        float *dst = red + (warp * HEADS + 2 * c) * RED_ROW + 16 * mt + 2 * g8;
+        if (2 * c < HEADS) *reinterpret_cast<float2 *>(dst) = make_float2(o[mt][0] * w0, o[mt][2] * w0);
+        if (2 * c + 1 < HEADS) *reinterpret_cast<float2 *>(dst + RED_ROW) = make_float2(o[mt][1] * w1, o[mt][3] * w1);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < HEADS * DV; i += C::THREADS) {
-        const int h = i / DV, d = i % DV;
-        float M = -INFINITY;
+    if (threadIdx.x < HEADS) {  // the heads' maxima and sums
+        const int h = threadIdx.x;
+        float M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) M = fmaxf(M, ml[(w * 8 + h) * 2]);
-        float L = 0.f, O = 0.f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
             const float mw = ml[(w * 8 + h) * 2];
-            const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
-            L += f * ml[(w * 8 + h) * 2 + 1];
-            O += f * red[(w * HEADS + h) * DV + d];
+            // (a maximum of -inf goes with a sum of zero, or of NaN, which stays)
+            L += (mw == -INFINITY ? 0.f : fast_exp2(mw - M)) * ml[(w * 8 + h) * 2 + 1];
         }
-        cta[i] = O;
-        if (d == 0) cml[2 * h] = M, cml[2 * h + 1] = L;
+        cml[2 * h] = M, cml[2 * h + 1] = L;
     }
-    const int n_part = p.splits / p.cluster;
+    __syncthreads();
+    for (int i = threadIdx.x; i < HEADS * DV; i += C::THREADS) {
+        const float *src = red + i / DV * RED_ROW + i % DV;
+        float O = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) O += src[w * HEADS * RED_ROW];
+        cta[i] = O;
+    }
     if (p.cluster > 1) {
         cluster_sync();
-        // this CTA's share of the value dims, from every CTA of the cluster
-        const int share = DV / p.cluster, d0 = cluster_ctarank() * share;
+        // this CTA's share of the places, from every CTA of the cluster
         for (int i = threadIdx.x; i < HEADS * share; i += C::THREADS) {
-            const int h = i / share, d = d0 + i % share;
+            const int h = i / share, d = first + i % share;
             const uint32_t a_o = smem_u32(cta + h * DV + d), a_ml = smem_u32(cml + 2 * h);
             float mr[MAX_CLUSTER], lr[MAX_CLUSTER], orr[MAX_CLUSTER], M = -INFINITY, L = 0.f, O = 0.f;
 #pragma unroll
@@ -546,34 +571,35 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
                 const size_t slot = static_cast<size_t>(item) * n_part + split / p.cluster;
                 p.ws[slot * (HEADS * DV) + h * DV + d] = O;
                 float *wml = p.ws + static_cast<size_t>(p.hkv) * p.batch * n_part * (HEADS * DV) + slot * (2 * HEADS);
-                if (d == 0) wml[2 * h] = M, wml[2 * h + 1] = L;
+                if (d == 0) wml[2 * h] = M, wml[2 * h + 1] = L;  // (O by place)
             } else {
                 red[h * DV + d] = paged_head(O, L);
             }
         }
         cluster_sync();  // everyone has read everyone's sums: the CTAs may leave
-        if (n_part > 1) return;
-        for (int i = threadIdx.x; i < 4 * share; i += C::THREADS) {
-            const int hh = i / share, dd = d0 + i % share;
-            const size_t r = bg * 4 + hh;
-            p.out[r * DV + dd] = paged_output(red[hh * DV + dd], red[4 * DV + dd], __ldg(p.lambda + r), p.gate[r * DV + dd]);
-        }
-        return;
+    } else {
+        __syncthreads();
+        for (int i = threadIdx.x; i < HEADS * DV; i += C::THREADS) red[i] = paged_head(cta[i], cml[2 * (i / DV) + 1]);
+        __syncthreads();
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 4 * DV; i += C::THREADS) {
-        const int hh = i / DV, dd = i % DV;
-        const size_t r = bg * 4 + hh;
-        p.out[r * DV + dd] = paged_output(paged_head(cta[i], cml[2 * hh + 1]), paged_head(cta[4 * DV + dd], cml[9]),
-                                          __ldg(p.lambda + r), p.gate[r * DV + dd]);
+    if (n_part > 1) return;
+#pragma unroll
+    for (int j = 0; j < MAX_OUT; ++j) {
+        const int i = threadIdx.x + j * C::THREADS;
+        if (i < 4 * share) {
+            const int h = i / share, d = first + i % share;
+            p.out[(bg * 4 + h) * DV + dim_of<E4M3>(d)] =
+                paged_output(red[h * DV + d], red[4 * DV + d], lam_in[j], gate_in[j]);
+        }
     }
 }
 
-// Several clusters per item: their sums joined, one block of 128 threads (one per value dim) per item.
+// Several clusters per item: their sums joined, one block of 128 threads (one per place) per item.
+template <bool E4M3>
 __global__ void __launch_bounds__(dp::DV)
 gdla_decode_paged_combine_kernel(const __grid_constant__ PagedDecode p) {
     using namespace dp;
-    const int n_part = p.splits / p.cluster, d = threadIdx.x;
+    const int n_part = p.splits / p.cluster, d = threadIdx.x, dim = dim_of<E4M3>(d);
     const size_t slot0 = static_cast<size_t>(blockIdx.x) * n_part;
     const float *wml = p.ws + static_cast<size_t>(p.hkv) * p.batch * n_part * (HEADS * DV);
     float hv[HEADS];
@@ -592,7 +618,7 @@ gdla_decode_paged_combine_kernel(const __grid_constant__ PagedDecode p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const size_t r = static_cast<size_t>(blockIdx.x) * 4 + i;
-        p.out[r * DV + d] = paged_output(hv[i], hv[4], __ldg(p.lambda + r), p.gate[r * DV + d]);
+        p.out[r * DV + dim] = paged_output(hv[i], hv[4], __ldg(p.lambda + r), p.gate[r * DV + dim]);
     }
 }
 
@@ -646,7 +672,7 @@ static cudaError_t launch_decode_paged_as(const PagedDecode &p, cudaStream_t str
     e = cudaLaunchKernelEx(&cfg, gdla_decode_paged_kernel<E4M3, WARPS>, p);
     if (e != cudaSuccess) return e;
     if (p.splits > p.cluster) {
-        gdla_decode_paged_combine_kernel<<<static_cast<unsigned>(p.hkv) * p.batch, dp::DV, 0, stream>>>(p);
+        gdla_decode_paged_combine_kernel<E4M3><<<static_cast<unsigned>(p.hkv) * p.batch, dp::DV, 0, stream>>>(p);
         return cudaPeekAtLastError();
     }
     return cudaSuccess;
