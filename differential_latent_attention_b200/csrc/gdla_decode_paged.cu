@@ -44,21 +44,23 @@ __device__ __forceinline__ int dim_of(int place) {
 constexpr float kTrail = 4.f;  // a probability is at most 2^4; with a V scale's ratio of 2^8 it stays in f16
 constexpr float kScoreLog2 = 0.07216878364870322f * 1.4426950408889634f;  // log2(e) / sqrt(192)
 
-template <bool E4M3, int WARPS_>
+// Four warps per CTA and four CTAs per SM, or (WIDE, for few items) eight warps that have the SM to themselves
+// and copy twice as far ahead.
+template <bool E4M3, bool WIDE>
 struct Cfg {
-    static constexpr int WARPS = WARPS_, THREADS = 32 * WARPS_;
+    static constexpr int WARPS = WIDE ? 8 : 4, THREADS = 32 * WARPS, CTAS_PER_SM = WIDE ? 1 : 4;
     static constexpr int ELT = E4M3 ? 1 : 2;
     static constexpr int K_BYTES = BLOCK * DQK * ELT, V_BYTES = BLOCK * DV * ELT;
     static constexpr int STAGE = K_BYTES + V_BYTES;  // 5 or 10 KB
-    // blocks ahead: 10 KB in flight per warp either way, 16 warps per SM
-    static constexpr int STAGES = E4M3 ? 2 : 1;
+    // blocks ahead: 10 KB in flight per warp either way (20 KB if WIDE)
+    static constexpr int STAGES = (E4M3 ? 2 : 1) * (WIDE ? 2 : 1);
     static constexpr int RING = WARPS * STAGES * STAGE;
     static constexpr int RED = WARPS * HEADS * RED_ROW * 4;  // fp32 [WARPS][5][132], over the ring once it is done
     static constexpr int OFF_CTA = RING > RED ? RING : RED;        // fp32 [5][128]: this CTA's sums
     static constexpr int OFF_ML = OFF_CTA + HEADS * DV * 4;        // fp32 [WARPS][8][2], then [5][2] of the CTA
     static constexpr int OFF_AUX = OFF_ML + (WARPS + 1) * 64;      // float4 per stage: position, page, scales
     static constexpr int SMEM_BYTES = OFF_AUX + WARPS * STAGES * 16;
-    static_assert(16 / WARPS * (SMEM_BYTES + 1024) <= 233472, "16 warps per SM");
+    static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 233472 && SMEM_BYTES <= 232448, "shared memory per SM");
 };
 
 // Shared-memory places of a block's rows: 16-byte units, permuted so that the eight lanes of a
@@ -207,12 +209,12 @@ __device__ __forceinline__ float paged_head(float O, float l) { return l == 0.f 
 // multiplied. The warps join in shared memory, the cluster's CTAs in distributed shared
 // memory, where CTA r finishes a share of the value dims; where an item has several clusters
 // their sums are left to the combine kernel.
-template <bool E4M3, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
+template <bool E4M3, bool WIDE>
+__global__ void __launch_bounds__(dp::Cfg<E4M3, WIDE>::THREADS, dp::Cfg<E4M3, WIDE>::CTAS_PER_SM)
 gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
     using namespace dp;
-    using C = Cfg<E4M3, WARPS>;
-    constexpr int STAGES = C::STAGES;
+    using C = Cfg<E4M3, WIDE>;
+    constexpr int STAGES = C::STAGES, WARPS = C::WARPS;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g8 = lane >> 2, c = lane & 3;
@@ -622,21 +624,34 @@ gdla_decode_paged_combine_kernel(const __grid_constant__ PagedDecode p) {
     }
 }
 
-// How an item is cut. Every CTA gets at least 16 blocks (four per warp) where the sizes allow
-// it: fewer and starting up and joining costs more than the copies.
+// How an item is cut, by measurement (us a call, 64-token pages; a cluster of n CTAs: "n", of 8 with m
+// parts joined by the combine kernel: "8 x m"):
+//  - few items: clusters as long as two CTAs per SM are not there yet and each gets a block per warp.
+//    1 x 16 heads x 4,096 bf16: 69.6 (1), 39.3 (2), 23.1 (4), 15.7 (8); 4 x 16 x 4,096: 72, 43, 32.0 (4), 32.6 (8)
+//  - many items: runs of 2,048 keys even out unequal lengths. 64 x 16 x 1,024 to 32,768 e4m3: 932 (2), 862 (4, 8);
+//    16 x 16 x 2,048 bf16: 55.2 (1), 57.9 (2)
+//  - the combine kernel costs some 5 us, so parts come with 4,096 keys each. 1 x 16 x 16,384 bf16: 44.0 (8),
+//    38.6 (8 x 2); 1 x 16 x 4,096: 15.9 (8), 20.2 (8 x 2)
+//  - up to 8 items: WIDE CTAs, whose clusters still find room side by side. 1 x 2 x 8,192 bf16: 21.4 (8), 16.5 (8 x 4),
+//    WIDE 13.8 (8); 1 x 1 x 32,768: 23.0 (8 x 8), WIDE 21.0 (8 x 4); but 1 x 16 x 4,096: 15.7 (8), WIDE 19.6 (8)
 PagedSplit paged_split(int batch, int hkv, int max_seqlen_k, int window, int sinks) {
     const long long items = static_cast<long long>(batch) * hkv;
     const long long keys = window > 0 ? std::min<long long>(max_seqlen_k, static_cast<long long>(window) + sinks)
                                       : max_seqlen_k;
     const long long blocks = (keys + dp::BLOCK - 1) / dp::BLOCK;
-    const long long most = std::max<long long>(1, blocks / 16);
-    // long contexts: runs of about 1,024 keys even out unequal lengths; few items: fill the card
-    long long want = std::max(blocks / 64, (2ll * kPlanSms + items - 1) / items);
-    want = std::min(want, most);
-    PagedSplit s{1, 1};
-    while (s.cluster < dp::MAX_CLUSTER && s.cluster * 2 <= want) s.cluster *= 2;
-    if (s.cluster == dp::MAX_CLUSTER && items * dp::MAX_CLUSTER < kPlanSms * 3 / 4)
-        s.parts = static_cast<int>(std::max<long long>(1, std::min<long long>(want / dp::MAX_CLUSTER, 16)));
+    PagedSplit s{1, 1, false};
+    if (items <= 8 && blocks >= 256) {
+        s.wide = true;
+        s.cluster = dp::MAX_CLUSTER;
+        s.parts = static_cast<int>(std::max<long long>(1, std::min(blocks / 512, 8 / items)));
+        return s;
+    }
+    while (s.cluster < dp::MAX_CLUSTER && s.cluster * 2 <= blocks / 4 &&
+           (items * s.cluster * 2 <= 2 * kPlanSms || s.cluster * 2 <= blocks / 128))
+        s.cluster *= 2;
+    if (s.cluster == dp::MAX_CLUSTER && items * dp::MAX_CLUSTER < kPlanSms)
+        s.parts = static_cast<int>(
+            std::max<long long>(1, std::min(blocks / 256, 2 * kPlanSms / (items * dp::MAX_CLUSTER))));
     return s;
 }
 
@@ -644,16 +659,16 @@ size_t paged_workspace_bytes(int batch, int hkv, const PagedSplit &s) {
     return s.parts > 1 ? static_cast<size_t>(batch) * hkv * s.parts * dp::HEADS * (dp::DV + 2) * sizeof(float) : 0;
 }
 
-template <bool E4M3, int WARPS>
+template <bool E4M3, bool WIDE>
 static cudaError_t launch_decode_paged_as(const PagedDecode &p, cudaStream_t stream) {
-    using C = dp::Cfg<E4M3, WARPS>;
+    using C = dp::Cfg<E4M3, WIDE>;
     static PerContextFlag attr_set;  // per device, for the context it was set in
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned long long ctx = current_context_id();
     if (!attr_set.is_set(dev, ctx)) {
-        e = cudaFuncSetAttribute(gdla_decode_paged_kernel<E4M3, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(gdla_decode_paged_kernel<E4M3, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         attr_set.set(dev, current_context_id());
@@ -669,7 +684,7 @@ static cudaError_t launch_decode_paged_as(const PagedDecode &p, cudaStream_t str
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, gdla_decode_paged_kernel<E4M3, WARPS>, p);
+    e = cudaLaunchKernelEx(&cfg, gdla_decode_paged_kernel<E4M3, WIDE>, p);
     if (e != cudaSuccess) return e;
     if (p.splits > p.cluster) {
         gdla_decode_paged_combine_kernel<E4M3><<<static_cast<unsigned>(p.hkv) * p.batch, dp::DV, 0, stream>>>(p);
@@ -679,9 +694,8 @@ static cudaError_t launch_decode_paged_as(const PagedDecode &p, cudaStream_t str
 }
 
 cudaError_t launch_decode_paged(const PagedDecode &p, bool e4m3, cudaStream_t stream) {
-    const bool wide = static_cast<long long>(p.hkv) * p.batch * p.splits < 2 * kPlanSms && p.cluster > 1;
-    if (e4m3) return wide ? launch_decode_paged_as<true, 8>(p, stream) : launch_decode_paged_as<true, 4>(p, stream);
-    return wide ? launch_decode_paged_as<false, 8>(p, stream) : launch_decode_paged_as<false, 4>(p, stream);
+    if (e4m3) return p.wide ? launch_decode_paged_as<true, true>(p, stream) : launch_decode_paged_as<true, false>(p, stream);
+    return p.wide ? launch_decode_paged_as<false, true>(p, stream) : launch_decode_paged_as<false, false>(p, stream);
 }
 
 }  // namespace gdla
