@@ -44,16 +44,14 @@ __device__ __forceinline__ int dim_of(int place) {
 constexpr float kTrail = 4.f;  // a probability is at most 2^4; with a V scale's ratio of 2^8 it stays in f16
 constexpr float kScoreLog2 = 0.07216878364870322f * 1.4426950408889634f;  // log2(e) / sqrt(192)
 
-// Four warps per CTA and four CTAs per SM, or (WIDE, for few items) eight warps that have the SM to themselves
-// and copy twice as far ahead.
+// Four warps per CTA and four CTAs per SM, or (WIDE, for few items) eight and two.
 template <bool E4M3, bool WIDE>
 struct Cfg {
-    static constexpr int WARPS = WIDE ? 8 : 4, THREADS = 32 * WARPS, CTAS_PER_SM = WIDE ? 1 : 4;
+    static constexpr int WARPS = WIDE ? 8 : 4, THREADS = 32 * WARPS, CTAS_PER_SM = WIDE ? 2 : 4;
     static constexpr int ELT = E4M3 ? 1 : 2;
     static constexpr int K_BYTES = BLOCK * DQK * ELT, V_BYTES = BLOCK * DV * ELT;
     static constexpr int STAGE = K_BYTES + V_BYTES;  // 5 or 10 KB
-    // blocks ahead: 10 KB in flight per warp either way (20 KB if WIDE)
-    static constexpr int STAGES = (E4M3 ? 2 : 1) * (WIDE ? 2 : 1);
+    static constexpr int STAGES = E4M3 ? 2 : 1;  // blocks ahead: 10 KB in flight per warp either way
     static constexpr int RING = WARPS * STAGES * STAGE;
     static constexpr int RED = WARPS * HEADS * RED_ROW * 4;  // fp32 [WARPS][5][132], over the ring once it is done
     static constexpr int OFF_CTA = RING > RED ? RING : RED;        // fp32 [5][128]: this CTA's sums
@@ -624,34 +622,32 @@ gdla_decode_paged_combine_kernel(const __grid_constant__ PagedDecode p) {
     }
 }
 
-// How an item is cut, by measurement (us a call, 64-token pages; a cluster of n CTAs: "n", of 8 with m
-// parts joined by the combine kernel: "8 x m"):
-//  - few items: clusters as long as two CTAs per SM are not there yet and each gets a block per warp.
-//    1 x 16 heads x 4,096 bf16: 69.6 (1), 39.3 (2), 23.1 (4), 15.7 (8); 4 x 16 x 4,096: 72, 43, 32.0 (4), 32.6 (8)
-//  - many items: runs of 2,048 keys even out unequal lengths. 64 x 16 x 1,024 to 32,768 e4m3: 932 (2), 862 (4, 8);
+// How an item is cut, by measurement (us a call, 64-token pages; "8 x 2": two clusters of 8 CTAs, joined by the
+// combine kernel):
+//  - up to 18 items: WIDE CTAs in clusters of 8, which then all run at once. batch 1, 16 heads, 4,096 tokens, bf16: 69.6 with
+//    one CTA per item, 15.5 with 8, 14.0 with 8 WIDE; 8 heads: 13.5 with 8, 10.8 WIDE; 3 x 16 heads: 25.9 with 8, 30.2 WIDE
+//  - the combine kernel costs some 5 us, so parts come with 8,192 keys each and only up to one CTA per SM. 1 x 1 x 32,768:
+//    42.9 (8 WIDE), 20.8 (8 x 4); 1 x 2 x 8,192: 15.4 (8), 15.1 (8 x 4); 1 x 16 x 16,384: 35.3 (8), 39.9 (8 x 2)
+//  - more items: clusters as long as two CTAs per SM are not there yet and each gets a block per warp.
+//    4 x 16 x 4,096: 72 (1), 43 (2), 32.0 (4), 32.6 (8)
+//  - many: runs of 2,048 keys even out unequal lengths. 64 x 16 x 1,024 to 32,768 e4m3: 932 (2), 862 (4, 8);
 //    16 x 16 x 2,048 bf16: 55.2 (1), 57.9 (2)
-//  - the combine kernel costs some 5 us, so parts come with 4,096 keys each. 1 x 16 x 16,384 bf16: 44.0 (8),
-//    38.6 (8 x 2); 1 x 16 x 4,096: 15.9 (8), 20.2 (8 x 2)
-//  - up to 8 items: WIDE CTAs, whose clusters still find room side by side. 1 x 2 x 8,192 bf16: 21.4 (8), 16.5 (8 x 4),
-//    WIDE 13.8 (8); 1 x 1 x 32,768: 23.0 (8 x 8), WIDE 21.0 (8 x 4); but 1 x 16 x 4,096: 15.7 (8), WIDE 19.6 (8)
 PagedSplit paged_split(int batch, int hkv, int max_seqlen_k, int window, int sinks) {
     const long long items = static_cast<long long>(batch) * hkv;
     const long long keys = window > 0 ? std::min<long long>(max_seqlen_k, static_cast<long long>(window) + sinks)
                                       : max_seqlen_k;
     const long long blocks = (keys + dp::BLOCK - 1) / dp::BLOCK;
     PagedSplit s{1, 1, false};
-    if (items <= 8 && blocks >= 256) {
+    if (items * dp::MAX_CLUSTER <= kPlanSms && blocks >= 64) {
         s.wide = true;
         s.cluster = dp::MAX_CLUSTER;
-        s.parts = static_cast<int>(std::max<long long>(1, std::min(blocks / 512, 8 / items)));
+        s.parts = static_cast<int>(
+            std::max<long long>(1, std::min(blocks / 512, kPlanSms / (items * dp::MAX_CLUSTER))));
         return s;
     }
     while (s.cluster < dp::MAX_CLUSTER && s.cluster * 2 <= blocks / 4 &&
            (items * s.cluster * 2 <= 2 * kPlanSms || s.cluster * 2 <= blocks / 128))
         s.cluster *= 2;
-    if (s.cluster == dp::MAX_CLUSTER && items * dp::MAX_CLUSTER < kPlanSms)
-        s.parts = static_cast<int>(
-            std::max<long long>(1, std::min(blocks / 256, 2 * kPlanSms / (items * dp::MAX_CLUSTER))));
     return s;
 }
 

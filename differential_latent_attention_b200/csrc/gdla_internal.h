@@ -278,7 +278,7 @@ struct PagedDecode {
 };
 struct PagedSplit {
     int cluster, parts;  // CTAs per cluster, clusters per (sequence, KV head)
-    bool wide;           // eight warps per CTA, one CTA per SM
+    bool wide;           // eight warps per CTA
 };
 PagedSplit paged_split(int batch, int hkv, int max_seqlen_k, int window, int sinks);
 size_t paged_workspace_bytes(int batch, int hkv, const PagedSplit &split);
