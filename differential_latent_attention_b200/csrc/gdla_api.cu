@@ -831,7 +831,7 @@ gdla_status_t gdla_attn_decode_paged(const void *q_sig, const void *q_noise, con
     p.ws = static_cast<float *>(workspace);
     p.splits = split.cluster * split.parts;
     p.cluster = split.cluster;
-    p.wide = split.wide;
+    p.warps = split.warps;
     p.page_shift = shift_of(page_size);
     p.q_sig = static_cast<const __nv_bfloat16 *>(q_sig);
     p.q_noise = static_cast<const __nv_bfloat16 *>(q_noise);

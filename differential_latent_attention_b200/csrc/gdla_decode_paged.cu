@@ -44,10 +44,11 @@ __device__ __forceinline__ int dim_of(int place) {
 constexpr float kTrail = 4.f;  // a probability is at most 2^4; with a V scale's ratio of 2^8 it stays in f16
 constexpr float kScoreLog2 = 0.07216878364870322f * 1.4426950408889634f;  // log2(e) / sqrt(192)
 
-// Four warps per CTA and four CTAs per SM, or (WIDE, for few items) eight and two.
-template <bool E4M3, bool WIDE>
+// Warps per CTA: 4, or 8 for few items, or 2 for many of few keys each (then a warp's own start and end weigh more
+// than its blocks). 14 to 16 warps per SM.
+template <bool E4M3, int WARPS_>
 struct Cfg {
-    static constexpr int WARPS = WIDE ? 8 : 4, THREADS = 32 * WARPS, CTAS_PER_SM = WIDE ? 2 : 4;
+    static constexpr int WARPS = WARPS_, THREADS = 32 * WARPS, CTAS_PER_SM = WARPS == 2 ? 7 : 16 / WARPS;
     static constexpr int ELT = E4M3 ? 1 : 2;
     static constexpr int K_BYTES = BLOCK * DQK * ELT, V_BYTES = BLOCK * DV * ELT;
     static constexpr int STAGE = K_BYTES + V_BYTES;  // 5 or 10 KB
@@ -207,12 +208,12 @@ __device__ __forceinline__ float paged_head(float O, float l) { return l == 0.f 
 // multiplied. The warps join in shared memory, the cluster's CTAs in distributed shared
 // memory, where CTA r finishes a share of the value dims; where an item has several clusters
 // their sums are left to the combine kernel.
-template <bool E4M3, bool WIDE>
-__global__ void __launch_bounds__(dp::Cfg<E4M3, WIDE>::THREADS, dp::Cfg<E4M3, WIDE>::CTAS_PER_SM)
+template <bool E4M3, int WARPS>
+__global__ void __launch_bounds__(dp::Cfg<E4M3, WARPS>::THREADS, dp::Cfg<E4M3, WARPS>::CTAS_PER_SM)
 gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
     using namespace dp;
-    using C = Cfg<E4M3, WIDE>;
-    constexpr int STAGES = C::STAGES, WARPS = C::WARPS;
+    using C = Cfg<E4M3, WARPS>;
+    constexpr int STAGES = C::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g8 = lane >> 2, c = lane & 3;
@@ -480,8 +481,8 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
     }
     cp_async_wait<0>();
 
-    // What this thread will need of gate and lambda, under way while the sums are joined: outputs (signal head,
-    // place) i = thread, thread + THREADS, ..
+    // What this thread will need of gate and lambda, under way while the sums are joined: outputs (place, signal
+    // head) i = thread, thread + THREADS, ..
     const int n_part = p.splits / p.cluster;
     const int share = DV / p.cluster, first = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) * share : 0;
     constexpr int MAX_OUT = 4 * DV / C::THREADS;
@@ -492,8 +493,9 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
         for (int j = 0; j < MAX_OUT; ++j) {
             const int i = threadIdx.x + j * C::THREADS;
             if (i < 4 * share) {
-                const size_t row = bg * 4 + i / share;
-                gate_in[j] = p.gate[row * DV + dim_of<E4M3>(first + i % share)];
+                const int h = p.cluster > 1 ? i / share : i / DV, at = p.cluster > 1 ? i - h * share : i % DV;
+                const size_t row = bg * 4 + h;
+                gate_in[j] = p.gate[row * DV + dim_of<E4M3>(first + at)];
                 lam_in[j] = __ldg(p.lambda + row);
             }
         }
@@ -537,16 +539,33 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
         cml[2 * h] = M, cml[2 * h + 1] = L;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < HEADS * DV; i += C::THREADS) {
-        const float *src = red + i / DV * RED_ROW + i % DV;
+    const auto warps_sum = [&](int h, int d) {
+        const float *src = red + h * RED_ROW + d;
         float O = 0.f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) O += src[w * HEADS * RED_ROW];
-        cta[i] = O;
+        return O;
+    };
+    if (p.cluster == 1) {
+        // (THREADS divides 128 or is its multiple, so a thread's outputs are those of one place or two)
+        constexpr int PLACES = MAX_OUT >= 4 ? MAX_OUT / 4 : 1;
+#pragma unroll
+        for (int q = 0; q < PLACES; ++q) {
+            const int d = (threadIdx.x + q * C::THREADS) % DV;
+            const float hn = paged_head(warps_sum(4, d), cml[9]);
+#pragma unroll
+            for (int j = q; j < MAX_OUT; j += PLACES) {
+                const int h = (threadIdx.x + j * C::THREADS) / DV;
+                p.out[(bg * 4 + h) * DV + dim_of<E4M3>(d)] =
+                    paged_output(paged_head(warps_sum(h, d), cml[2 * h + 1]), hn, lam_in[j], gate_in[j]);
+            }
+        }
+        return;
     }
-    if (p.cluster > 1) {
-        cluster_sync();
-        // this CTA's share of the places, from every CTA of the cluster
+    for (int i = threadIdx.x; i < HEADS * DV; i += C::THREADS) cta[i] = warps_sum(i / DV, i % DV);
+    cluster_sync();
+    // this CTA's share of the places, from every CTA of the cluster
+    {
         for (int i = threadIdx.x; i < HEADS * share; i += C::THREADS) {
             const int h = i / share, d = first + i % share;
             const uint32_t a_o = smem_u32(cta + h * DV + d), a_ml = smem_u32(cml + 2 * h);
@@ -577,10 +596,6 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
             }
         }
         cluster_sync();  // everyone has read everyone's sums: the CTAs may leave
-    } else {
-        __syncthreads();
-        for (int i = threadIdx.x; i < HEADS * DV; i += C::THREADS) red[i] = paged_head(cta[i], cml[2 * (i / DV) + 1]);
-        __syncthreads();
     }
     if (n_part > 1) return;
 #pragma unroll
@@ -624,12 +639,14 @@ gdla_decode_paged_combine_kernel(const __grid_constant__ PagedDecode p) {
 
 // How an item is cut, by measurement (us a call, 64-token pages; "8 x 2": two clusters of 8 CTAs, joined by the
 // combine kernel):
-//  - up to 18 items: WIDE CTAs in clusters of 8, which then all run at once. batch 1, 16 heads, 4,096 tokens, bf16: 69.6 with
-//    one CTA per item, 15.5 with 8, 14.0 with 8 WIDE; 8 heads: 13.5 with 8, 10.8 WIDE; 3 x 16 heads: 25.9 with 8, 30.2 WIDE
+//  - up to 18 items: CTAs of 8 warps in clusters of 8, which then all run at once. batch 1, 16 heads, 4,096 tokens, bf16:
+//    69.6 with one CTA of 4 warps per item, 15.5 with 8, 14.0 with 8 of 8 warps; 8 heads: 13.5 and 10.8; 3 x 16 heads: 25.9
+//    and 30.2
 //  - the combine kernel costs some 5 us, so parts come with 8,192 keys each and only up to one CTA per SM. 1 x 1 x 32,768:
-//    42.9 (8 WIDE), 20.8 (8 x 4); 1 x 2 x 8,192: 15.4 (8), 15.1 (8 x 4); 1 x 16 x 16,384: 35.3 (8), 39.9 (8 x 2)
+//    42.9 (8), 20.8 (8 x 4); 1 x 2 x 8,192: 15.4 (8), 15.1 (8 x 4); 1 x 16 x 16,384: 35.3 (8), 39.9 (8 x 2)
 //  - more items: clusters as long as two CTAs per SM are not there yet and each gets a block per warp.
 //    4 x 16 x 4,096: 72 (1), 43 (2), 32.0 (4), 32.6 (8)
+//  - many of few keys (windows): CTAs of 2 warps. 64 x 16, window 128 and 4 sinks, bf16: 28.4 with 4 warps, 22.4 with 2
 //  - many: runs of 2,048 keys even out unequal lengths. 64 x 16 x 1,024 to 32,768 e4m3: 932 (2), 862 (4, 8);
 //    16 x 16 x 2,048 bf16: 55.2 (1), 57.9 (2)
 PagedSplit paged_split(int batch, int hkv, int max_seqlen_k, int window, int sinks) {
@@ -637,9 +654,9 @@ PagedSplit paged_split(int batch, int hkv, int max_seqlen_k, int window, int sin
     const long long keys = window > 0 ? std::min<long long>(max_seqlen_k, static_cast<long long>(window) + sinks)
                                       : max_seqlen_k;
     const long long blocks = (keys + dp::BLOCK - 1) / dp::BLOCK;
-    PagedSplit s{1, 1, false};
+    PagedSplit s{1, 1, 4};
     if (items * dp::MAX_CLUSTER <= kPlanSms && blocks >= 64) {
-        s.wide = true;
+        s.warps = 8;
         s.cluster = dp::MAX_CLUSTER;
         s.parts = static_cast<int>(
             std::max<long long>(1, std::min(blocks / 512, kPlanSms / (items * dp::MAX_CLUSTER))));
@@ -648,6 +665,7 @@ PagedSplit paged_split(int batch, int hkv, int max_seqlen_k, int window, int sin
     while (s.cluster < dp::MAX_CLUSTER && s.cluster * 2 <= blocks / 4 &&
            (items * s.cluster * 2 <= 2 * kPlanSms || s.cluster * 2 <= blocks / 128))
         s.cluster *= 2;
+    if (s.cluster == 1 && blocks <= 32 && items > 4 * kPlanSms) s.warps = 2;
     return s;
 }
 
@@ -655,16 +673,16 @@ size_t paged_workspace_bytes(int batch, int hkv, const PagedSplit &s) {
     return s.parts > 1 ? static_cast<size_t>(batch) * hkv * s.parts * dp::HEADS * (dp::DV + 2) * sizeof(float) : 0;
 }
 
-template <bool E4M3, bool WIDE>
+template <bool E4M3, int WARPS>
 static cudaError_t launch_decode_paged_as(const PagedDecode &p, cudaStream_t stream) {
-    using C = dp::Cfg<E4M3, WIDE>;
+    using C = dp::Cfg<E4M3, WARPS>;
     static PerContextFlag attr_set;  // per device, for the context it was set in
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned long long ctx = current_context_id();
     if (!attr_set.is_set(dev, ctx)) {
-        e = cudaFuncSetAttribute(gdla_decode_paged_kernel<E4M3, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(gdla_decode_paged_kernel<E4M3, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         attr_set.set(dev, current_context_id());
@@ -680,7 +698,7 @@ static cudaError_t launch_decode_paged_as(const PagedDecode &p, cudaStream_t str
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, gdla_decode_paged_kernel<E4M3, WIDE>, p);
+    e = cudaLaunchKernelEx(&cfg, gdla_decode_paged_kernel<E4M3, WARPS>, p);
     if (e != cudaSuccess) return e;
     if (p.splits > p.cluster) {
         gdla_decode_paged_combine_kernel<E4M3><<<static_cast<unsigned>(p.hkv) * p.batch, dp::DV, 0, stream>>>(p);
@@ -689,9 +707,17 @@ static cudaError_t launch_decode_paged_as(const PagedDecode &p, cudaStream_t str
     return cudaSuccess;
 }
 
+template <bool E4M3>
+static cudaError_t launch_decode_paged_of(const PagedDecode &p, cudaStream_t stream) {
+    switch (p.warps) {
+        case 2: return launch_decode_paged_as<E4M3, 2>(p, stream);
+        case 4: return launch_decode_paged_as<E4M3, 4>(p, stream);
+        default: return launch_decode_paged_as<E4M3, 8>(p, stream);
+    }
+}
+
 cudaError_t launch_decode_paged(const PagedDecode &p, bool e4m3, cudaStream_t stream) {
-    if (e4m3) return p.wide ? launch_decode_paged_as<true, true>(p, stream) : launch_decode_paged_as<true, false>(p, stream);
-    return p.wide ? launch_decode_paged_as<false, true>(p, stream) : launch_decode_paged_as<false, false>(p, stream);
+    return e4m3 ? launch_decode_paged_of<true>(p, stream) : launch_decode_paged_of<false>(p, stream);
 }
 
 }  // namespace gdla

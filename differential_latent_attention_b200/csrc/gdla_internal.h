@@ -274,11 +274,12 @@ struct PagedDecode {
     float *ws;
     int num_pages, page_size, page_shift, max_pages, max_seqlen_k, batch, hkv, window, sinks;
     int splits, cluster;  // CTAs per (sequence, KV head), and how many of them form a cluster
-    bool rotate, wide;
+    int warps;            // per CTA: 2, 4 or 8
+    bool rotate;
 };
 struct PagedSplit {
     int cluster, parts;  // CTAs per cluster, clusters per (sequence, KV head)
-    bool wide;           // eight warps per CTA
+    int warps;           // per CTA
 };
 PagedSplit paged_split(int batch, int hkv, int max_seqlen_k, int window, int sinks);
 size_t paged_workspace_bytes(int batch, int hkv, const PagedSplit &split);

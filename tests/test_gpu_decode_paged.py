@@ -70,6 +70,14 @@ def test_every_way_to_cut_an_item(kind):
     _check([9000], 1, 128, kind, 406, most=70000)                             # planned for more than is there
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_many_items_of_few_keys(kind):
+    """More than 592 items of at most 512 keys: CTAs of two warps."""
+    lens = [(37 * i) % 401 for i in range(200)]
+    _check(lens, 3, 16, kind, 441)
+    _check([n + 500 for n in lens], 4, 32, kind, 442, window=100, sinks=17, rotate=True)
+
+
 def test_sixty_four_heads():
     _check([500, 33], 64, 32, "e4m3", 450)
     _check([500, 33], 64, 32, "bf16", 451)
