@@ -139,11 +139,11 @@ __device__ __forceinline__ RopePart rope_part(const AppendPlan &p, int token, in
     if (p.rotate) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float c, s;
+            double c, s;
             rotary_angle(pos, 8 * q + i, c, s);
-            const float x = r.lo[i], y = r.hi[i];
-            r.lo[i] = x * c - y * s;
-            r.hi[i] = x * s + y * c;
+            const double x = r.lo[i], y = r.hi[i];
+            r.lo[i] = static_cast<float>(x * c - y * s);
+            r.hi[i] = static_cast<float>(x * s + y * c);
         }
     }
     return r;
@@ -303,7 +303,7 @@ gdla_cache_append_kernel(const __grid_constant__ AppendPlan p) {
 }
 
 // Few tokens per sequence (a decode step): one warp per (unit, head), row by row; lanes 0..15 hold
-// a row's K content, 16..31 its V, and lanes 0..3 the rotary part as well.
+// a row's K content, 16..31 its V, and lane i pair i of the rotary part as well.
 template <bool E4M3>
 __global__ void __launch_bounds__(128)
 gdla_cache_append_step_kernel(const __grid_constant__ AppendPlan p, int units) {
@@ -317,40 +317,51 @@ gdla_cache_append_step_kernel(const __grid_constant__ AppendPlan p, int units) {
     const __nv_bfloat16 *src = is_k ? p.k_nope + static_cast<size_t>(a.tok0) * p.nope_token + h * p.nope_head + 8 * lane
                                     : p.v + static_cast<size_t>(a.tok0) * p.v_token + h * p.v_head + 8 * (lane - 16);
     const long long step = is_k ? p.nope_token : p.v_token;
-    const auto piece = [&](int r) { return __ldg(reinterpret_cast<const uint4 *>(src + r * step)); };
-    const auto turned = [&](int r) { return rope_part(p, a.tok0 + r, a.pos0 + a.slot0 + r, lane & 3); };
-    // the last row (of a step: the only one) is under way while the page's entry comes
-    uint4 x0 = piece(n - 1);
-    RopePart q0;
-    if (lane < 4) q0 = turned(n - 1);
+    struct Row {
+        uint4 x;       // this lane's eight values of K's content or V
+        float lo, hi;  // its rotary pair
+    };
+    const auto fetch = [&](int r) {
+        Row y;
+        y.x = __ldg(reinterpret_cast<const uint4 *>(src + r * step));
+        const __nv_bfloat16 *rope = p.k_rope + static_cast<size_t>(a.tok0 + r) * p.rope_token + lane;
+        y.lo = __bfloat162float(rope[0]);
+        y.hi = __bfloat162float(rope[32]);
+        if (p.rotate) {
+            double c, s;
+            rotary_angle(a.pos0 + a.slot0 + r, lane, c, s);
+            const double lo = y.lo, hi = y.hi;
+            y.lo = static_cast<float>(lo * c - hi * s);
+            y.hi = static_cast<float>(lo * s + hi * c);
+        }
+        return y;
+    };
+    Row row = fetch(n - 1);  // the last row (of a step: the only one) is under way while the page's entry comes
     if (!in_pool(p, a.page)) return;
     const size_t blk = static_cast<size_t>(a.page) * p.hkv + h, slot = (blk << p.page_shift) + a.slot0;
     if constexpr (!E4M3) {
         __nv_bfloat16 *kd = static_cast<__nv_bfloat16 *>(p.k_pages) + slot * 192;
         __nv_bfloat16 *vd = static_cast<__nv_bfloat16 *>(p.v_pages) + slot * 128;
         for (int r = n - 1; r >= 0; --r) {
-            const uint4 x = r < n - 1 ? piece(r) : x0;
-            *reinterpret_cast<uint4 *>(is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16)) = x;
-            if (lane < 4) {
-                const RopePart q = r < n - 1 ? turned(r) : q0;
-                *reinterpret_cast<uint4 *>(kd + r * 192 + 128 + 8 * lane) = to_bf16(q.lo);
-                *reinterpret_cast<uint4 *>(kd + r * 192 + 160 + 8 * lane) = to_bf16(q.hi);
-            }
+            if (r < n - 1) row = fetch(r);
+            *reinterpret_cast<uint4 *>(is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16)) = row.x;
+            kd[r * 192 + 128 + lane] = __float2bfloat16_rn(row.lo);
+            kd[r * 192 + 160 + lane] = __float2bfloat16_rn(row.hi);
         }
     } else {
         const bool goes_on = a.slot0 > 0;
         const float k_had = goes_on ? p.k_scale[blk] : 0.f, v_had = goes_on ? p.v_scale[blk] : 0.f;
         uint32_t km = 0u, vm = 0u;
-        for (int r = 0; r < n; ++r) {  // the last row stays for the writing: with one row nothing is read twice
-            if (n > 1) x0 = piece(r);
-            const uint32_t raw = max_bits(x0);
-            const uint32_t m = raw < kInfBits ? raw : finite_max_bits(x0);
-            if (is_k) km = max(km, m); else vm = max(vm, m);
-            if (lane < 4) {
-                if (n > 1) q0 = turned(r);
-                km = max(km, max(max_bits(q0.lo, true), max_bits(q0.hi, true)));
-            }
-        }
+        const auto largest = [&](const Row &y) {
+            const uint32_t raw = max_bits(y.x), m = raw < kInfBits ? raw : finite_max_bits(y.x);
+            if (is_k)
+                km = max(km, m);
+            else
+                vm = max(vm, m);
+            km = max(km, __float_as_uint(fmaxf(finite_abs(y.lo), finite_abs(y.hi))));
+        };
+        largest(row);  // it stays for the writing: with one row nothing is read twice
+        for (int r = 0; r < n - 1; ++r) largest(fetch(r));
         km = __reduce_max_sync(0xffffffffu, km);
         vm = __reduce_max_sync(0xffffffffu, vm);
         float k_shrink, v_shrink;
@@ -362,16 +373,12 @@ gdla_cache_append_step_kernel(const __grid_constant__ AppendPlan p, int units) {
         if (v_shrink < 1.f) shrink_codes(vd - a.slot0 * 128, a.slot0 * 128, v_shrink, lane, 32);
         const float ki = power_of_two(-ke), vi = power_of_two(-ve);
         for (int r = n - 1; r >= 0; --r) {
-            if (r < n - 1) {
-                x0 = piece(r);
-                if (lane < 4) q0 = turned(r);
-            }
+            if (r < n - 1) row = fetch(r);
             uint8_t *dst = is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16);
-            *reinterpret_cast<uint2 *>(dst) = to_e4m3<false>(x0, is_k ? ki : vi);
-            if (lane < 4) {
-                *reinterpret_cast<uint2 *>(kd + r * 192 + 128 + 8 * lane) = to_e4m3<false>(q0.lo, ki);
-                *reinterpret_cast<uint2 *>(kd + r * 192 + 160 + 8 * lane) = to_e4m3<false>(q0.hi, ki);
-            }
+            *reinterpret_cast<uint2 *>(dst) = to_e4m3<false>(row.x, is_k ? ki : vi);
+            const uint32_t two = pair_e4m3<false>(row.lo, row.hi, ki);
+            kd[r * 192 + 128 + lane] = static_cast<uint8_t>(two);
+            kd[r * 192 + 160 + lane] = static_cast<uint8_t>(two >> 8);
         }
         if (lane == 0 && (k_had != power_of_two(ke) || v_had != power_of_two(ve)))
             p.k_scale[blk] = power_of_two(ke), p.v_scale[blk] = power_of_two(ve);

@@ -24,7 +24,13 @@ __constant__ double kRotaryTurns[32] = {
     5.0329212104487035e-05, 3.774158471741977e-05, 2.8302195830623396e-05, 2.122365276477766e-05,
 };
 
-// cos and sin of the rotary angle of pair i at a position.
+// cos and sin of the rotary angle of pair i at a position. In fp64 for keys, which are rounded once, to the
+// cache's type, after the turn: an fp32 cosine, off by 2^-24, takes one turned value in a million to the e4m3
+// code beside its own. Queries, which meet f16 or split bf16 next, have it in fp32.
+__device__ __forceinline__ void rotary_angle(int position, int pair, double &c, double &s) {
+    const double turns = static_cast<double>(position) * kRotaryTurns[pair];
+    sincospi(2.0 * (turns - rint(turns)), &s, &c);
+}
 __device__ __forceinline__ void rotary_angle(int position, int pair, float &c, float &s) {
     const double turns = static_cast<double>(position) * kRotaryTurns[pair];
     sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
