@@ -406,8 +406,13 @@ cudaError_t launch_cache_append(const AppendPlan &plan, bool e4m3, cudaStream_t 
             gdla_cache_append_step_kernel<false><<<grid, 128, 0, stream>>>(p, static_cast<int>(units));
         return cudaPeekAtLastError();
     }
-    // heads of a CTA: as many as share the rotary part while the card still gets several CTAs per SM
-    p.heads_per_cta = static_cast<int>(std::min<long long>(4, std::max<long long>(1, units * p.hkv / (8 * kPlanSms))));
+    // Heads of a CTA: 128 rows' worth (fewer and the search and the turned keys weigh more, us at 1, 2, 4, 8 heads: 13 chunks
+    // of 400 tokens, 5 heads, bf16 pages of 16: 13.3, 11.2, 8.8, 7.6; 8,000 tokens, 16 heads, e4m3 pages of 32: 40, 32, 30, 33),
+    // four at least in large calls (32,600 tokens, e4m3 pages of 64: 119, 91, 82, 83), as long as every SM gets a CTA.
+    const long long pairs = units * p.hkv;
+    long long heads = 128 / p.page_size;
+    if (pairs >= 32ll * kPlanSms) heads = std::max(heads, 4ll);
+    p.heads_per_cta = static_cast<int>(std::max(1ll, std::min(heads, std::min<long long>(p.hkv, pairs / kPlanSms))));
     const unsigned grid = static_cast<unsigned>(units * ((p.hkv + p.heads_per_cta - 1) / p.heads_per_cta));
     if (e4m3)
         launch_append_pages<true>(p, grid, stream);
