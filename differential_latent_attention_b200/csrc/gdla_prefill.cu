@@ -270,24 +270,46 @@ __device__ __forceinline__ void epi_chunk_staged(const uint32_t (&o)[32], float 
 // row statistics lse2 = m + log2(l) (so P = exp2(s log2(e)/sqrt(192) - lse2))
 // and rowsum(dH * H) taken with that rounded dH.
 // The rows of gate and dout are read a 32-column chunk ahead: the first before the wait for the item's last
-// product, each next one while a chunk is computed.
+// product, each next one while a chunk is computed. `wide`: every buffer involved is 32-byte aligned, and each lane
+// moves whole sectors.
 struct BwdRow {
-    uint4 g[4], go[4];
+    uint32_t g[16], go[16];
 };
-__device__ __forceinline__ void epi_bwd_fetch(bool sig, size_t srow, const __nv_bfloat16 *__restrict__ gate,
-                                              const __nv_bfloat16 *__restrict__ dout, int ch, BwdRow &row) {
+__device__ __forceinline__ void row_load(const __nv_bfloat16 *src, bool wide, uint32_t (&x)[16]) {
+    if (wide) {
+        ld_nc_v8(src, x);
+        ld_nc_v8(src + 16, x + 8);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        row.g[i] = row.go[i] = make_uint4(0, 0, 0, 0);
-        if (sig) {
-            row.g[i] = __ldg(reinterpret_cast<const uint4 *>(gate + srow * DV + ch * 32) + i);
-            row.go[i] = __ldg(reinterpret_cast<const uint4 *>(dout + srow * DV + ch * 32) + i);
+        for (int i = 0; i < 4; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+            x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
         }
+    }
+}
+__device__ __forceinline__ void row_store(__nv_bfloat16 *dst, bool wide, const uint32_t (&x)[16]) {
+    if (wide) {
+        st_v8(dst, x);
+        st_v8(dst + 16, x + 8);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    }
+}
+__device__ __forceinline__ void epi_bwd_fetch(bool sig, size_t srow, const __nv_bfloat16 *__restrict__ gate,
+                                              const __nv_bfloat16 *__restrict__ dout, int ch, bool wide, BwdRow &row) {
+    if (sig) {
+        row_load(gate + srow * DV + ch * 32, wide, row.g);
+        row_load(dout + srow * DV + ch * 32, wide, row.go);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) row.g[i] = row.go[i] = 0u;
     }
 }
 __device__ __forceinline__ void epi_backward(uint32_t o_addr, float l_run, float m_run, bool is_sig, bool tok_valid,
                                              int lane, int hsrc, size_t tok, int hs, int hkv, int group, float lam,
-                                             BwdRow &next, const __nv_bfloat16 *__restrict__ gate,
+                                             BwdRow &next, bool wide, const __nv_bfloat16 *__restrict__ gate,
                                              const BwdIO &bwd) {
     const bool sig = is_sig && tok_valid;
     const bool noi = lane >= 24 && lane < 30 && tok_valid;
@@ -300,12 +322,8 @@ __device__ __forceinline__ void epi_backward(uint32_t o_addr, float l_run, float
     for (int ch = 0; ch < DV / 32; ++ch) {
         uint32_t o[32], g[16], go[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 a = next.g[i], c = next.go[i];
-            g[4 * i] = a.x, g[4 * i + 1] = a.y, g[4 * i + 2] = a.z, g[4 * i + 3] = a.w;
-            go[4 * i] = c.x, go[4 * i + 1] = c.y, go[4 * i + 2] = c.z, go[4 * i + 3] = c.w;
-        }
-        if (ch + 1 < DV / 32) epi_bwd_fetch(sig, srow, gate, bwd.dout, ch + 1, next);
+        for (int i = 0; i < 16; ++i) g[i] = next.g[i], go[i] = next.go[i];
+        if (ch + 1 < DV / 32) epi_bwd_fetch(sig, srow, gate, bwd.dout, ch + 1, wide, next);
         tmem_ld32(o_addr + ch * 32, o);
         uint32_t w_dgate[16], w_dh[16];
 #pragma unroll
@@ -331,18 +349,10 @@ __device__ __forceinline__ void epi_backward(uint32_t o_addr, float l_run, float
             drow += __uint_as_float(dh << 16) * h0 + __uint_as_float(dh & 0xFFFF0000u) * h1;
         }
         if (sig) {
-            uint4 *dg = reinterpret_cast<uint4 *>(bwd.dgate + srow * DV + ch * 32);
-            uint4 *dh = reinterpret_cast<uint4 *>(bwd.dh_sig + srow * DV + ch * 32);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dg[i] = make_uint4(w_dgate[4 * i], w_dgate[4 * i + 1], w_dgate[4 * i + 2], w_dgate[4 * i + 3]);
-                dh[i] = make_uint4(w_dh[4 * i], w_dh[4 * i + 1], w_dh[4 * i + 2], w_dh[4 * i + 3]);
-            }
+            row_store(bwd.dgate + srow * DV + ch * 32, wide, w_dgate);
+            row_store(bwd.dh_sig + srow * DV + ch * 32, wide, w_dh);
         } else if (noi) {
-            uint4 *dh = reinterpret_cast<uint4 *>(bwd.dh_noise + nrow * DV + ch * 32);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                dh[i] = make_uint4(w_dh[4 * i], w_dh[4 * i + 1], w_dh[4 * i + 2], w_dh[4 * i + 3]);
+            row_store(bwd.dh_noise + nrow * DV + ch * 32, wide, w_dh);
         }
     }
     if (sig) bwd.dlambda[srow] = dl;
@@ -688,7 +698,9 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const uint32_t o_addr = lane_base + C::O_COL0 + x * 128;
         const float c_log2 = 0.07216878364870322f * 1.4426950408889634f;  // log2(e) / sqrt(192)
-        const bool wide = ((reinterpret_cast<uintptr_t>(gate) | reinterpret_cast<uintptr_t>(out)) & 31u) == 0;
+        const bool wide = ((reinterpret_cast<uintptr_t>(gate) | reinterpret_cast<uintptr_t>(out) |
+                            (C::EPI == EPI_BWD ? reinterpret_cast<uintptr_t>(bwd.dout) | reinterpret_cast<uintptr_t>(bwd.dgate)
+                                               : uintptr_t(0))) & 31u) == 0;  // (the workspace's dH is 256-byte aligned)
         int sxs = 0;  // S/P steps of this q tile so far
         int pv = 0;   // PV products of this q tile so far (o_done phases)
         int n_item = 0;
@@ -897,7 +909,7 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
                 }
             } else if constexpr (C::EPI == EPI_BWD) {
                 BwdRow first;
-                epi_bwd_fetch(valid, row, gate, bwd.dout, 0, first);
+                epi_bwd_fetch(valid, row, gate, bwd.dout, 0, wide, first);
                 const float lam = valid ? __ldg(lambda + row) : 0.f;
                 if (!__all_sync(0xffffffffu, mbar_wait(o_final + x, n_item & 1, abort_flag, ERR_SITE_PREFILL | 9))) {
                     ok = false;
@@ -906,7 +918,7 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
                 tc_fence_after();
                 const size_t tok = static_cast<size_t>(it.s0 + t);
                 epi_backward(o_addr, l_run, m_run, is_sig, t < it.L, lane, hsrc, tok, hs, hkv, it.group, lam, first,
-                             gate, bwd);
+                             wide, gate, bwd);
             } else {
                 // Signal rows fetch their gate row and lambda before waiting for the last PV.
                 uint32_t gw[DV / 32][16];

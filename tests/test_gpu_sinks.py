@@ -203,6 +203,30 @@ def test_deterministic_own_buffers_and_streams():
         _bwd(t, dout, seqlens, window, sinks, workspace=ws[:need - 256])
 
 
+@pytest.mark.parametrize("window, sinks", [(64, 7), (300, 4), (64, 0)])
+def test_buffers_on_16_byte_boundaries(window, sinks):
+    """Every buffer 16 bytes past a 32-byte boundary: the same bits."""
+    seqlens = (500, 33)
+    t = gi.make_prefill_inputs(seqlens, 2, 18, device="cuda")
+    dout = gi.make_prefill_grad(seqlens, 2, 18, device="cuda")
+
+    def shift(x):
+        step = 16 // x.element_size()
+        y = torch.empty(x.numel() + 2 * step, dtype=x.dtype, device="cuda")
+        off = step if y.data_ptr() % 32 == 0 else 0
+        y = y[off:off + x.numel()].view(x.shape)
+        assert y.data_ptr() % 32 == 16
+        return y.copy_(x)
+
+    moved = {n: shift(x) for n, x in t.items()}
+    a = _bwd(t, dout, seqlens, window, sinks)
+    grads = {n: shift(x) for n, x in a.items()}
+    b = _bwd(moved, shift(dout), seqlens, window, sinks, grads=grads)
+    assert all(_same(a[n], b[n]) for n in GRADS)
+    out = shift(t["gate"])
+    assert _same(_fwd(moved, seqlens, window, sinks, out=out), _fwd(t, seqlens, window, sinks))
+
+
 def test_captured_forward_and_backward():
     seqlens, window, sinks = (700, 100), 128, 4
     t = gi.make_prefill_inputs(seqlens, 2, 16, device="cuda")
