@@ -552,12 +552,17 @@ static gdla_status_t attn_bwd(const void *q_sig, const void *q_noise, const void
 
 size_t gdla_attn_bwd_sinks_workspace_bytes(int batch, const int32_t *seqlens, int num_kv_heads, int window,
                                            int sinks) {
-    long long n_total = 0;
-    int longest = 0;
-    if (check_seqlens(batch, seqlens, num_kv_heads, &n_total, &longest) != GDLA_OK ||
-        check_sinks(longest, &window, &sinks) != GDLA_OK)
-        return 0;
-    return bwd_workspace(n_total, num_kv_heads, dkv_splits(batch, seqlens, num_kv_heads, window, sinks), sinks).total;
+    size_t total = 0;
+    (void)no_throw([&] {
+        long long n_total = 0;
+        int longest = 0;
+        gdla_status_t st = check_seqlens(batch, seqlens, num_kv_heads, &n_total, &longest);
+        if (st == GDLA_OK) st = check_sinks(longest, &window, &sinks);
+        if (st == GDLA_OK)
+            total = bwd_workspace(n_total, num_kv_heads, dkv_splits(batch, seqlens, num_kv_heads, window, sinks), sinks).total;
+        return st;
+    });
+    return total;
 }
 
 gdla_status_t gdla_attn_bwd(const void *q_sig, const void *q_noise, const void *k, const void *v,

@@ -9,7 +9,13 @@
 // amax <= 448 * 2^e over the tokens that the page holds. A page that goes on
 // keeps the larger of its scale and the new tokens' one; where it grows, the
 // codes that the page held are divided by the growth, which is exact but for codes
-// that fall under e4m3's subnormals.
+// that fall under e4m3's subnormals. A power of two costs e4m3 no precision (it is a floating type: a
+// scale moves only where its smallest numbers begin) and keeps those divisions exact.
+//
+// Bytes alone bound it: 8,320 read and 5,120 (e4m3, 16 heads) or 10,240 (bf16) written per token.
+// Measured on one B200 (16 heads): 32,600 tokens into e4m3 pages of 64 82.5 us, 5.3 TB/s of 6.5 TB/s copied, held
+// by the conversions beside the loads (59 % of the issue slots); a step of 64 sequences 4.3 us, of one 3.1 us, which
+// is a launch and a chain of five dependent loads (sequence, lengths, page, scale, row).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -347,8 +347,8 @@ GDLA_API gdla_status_t gdla_attn_decode_noalloc(const void *q_sig, const void *q
  * e4m3: scale = 2^e, the smallest (e >= -110) with amax <= 448 * 2^e over the finite
  * values of the page's tokens. A page that goes on keeps the larger of its own
  * scale and the new tokens'; if that grows, its older codes are rounded to the new
- * scale. A page whose slot 0 is written takes the new tokens' scale alone. NaN and
- * infinities become e4m3's NaN.
+ * scale (its own must be a power of two, as this call writes them). A page whose slot
+ * 0 is written takes the new tokens' scale alone. NaN and infinities become e4m3's NaN.
  * Slots that get no token, and pages that no sequence's new tokens fall in, are left
  * as they were. A sequence whose entries do not fit (a negative count or length, more
  * positions than its row of the table has, rows outside 0 .. num_new_tokens) and
