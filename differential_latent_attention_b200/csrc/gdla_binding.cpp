@@ -204,6 +204,7 @@ PyObject *attn_decode_paged(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         const auto on = launch_stream(a[16], c.dev);
         if (a[14] == Py_None) {
             made = at::empty_like(THPVariable_Unpack(a[8]));
+            if (a[16] != Py_None) made.record_stream(on);  // memory of the current stream, written on another
             out = made.data_ptr();
         } else {
             out = dense(a[14], "out", at::kBFloat16, {c.batch, hs, kDv}, c.dev);
@@ -218,7 +219,7 @@ PyObject *attn_decode_paged(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
             ws_bytes = w.nbytes();
         } else if ((ws_bytes = workspace_fn(static_cast<int>(c.batch), static_cast<int>(c.heads), most, window, sinks)) > 0) {
             scratch = at::empty({static_cast<int64_t>(ws_bytes)}, THPVariable_Unpack(a[8]).options().dtype(at::kByte));
-            if (a[16] != Py_None) scratch.record_stream(on);  // it may be handed on as soon as this returns
+            if (a[16] != Py_None) scratch.record_stream(on);
             ws = scratch.data_ptr();
         }
         gdla_status_t st;

@@ -383,7 +383,8 @@ GDLA_API gdla_status_t gdla_cache_append(const void *k_nope, long long k_nope_to
  *   workspace    DEVICE scratch of gdla_decode_paged_workspace_bytes(batch, num_kv_heads,
  *                max_seqlen_k, window, sinks) bytes, 256-byte aligned (may be NULL when that
  *                is 0: it is needed for few sequences and heads over long contexts alone);
- *                its contents need no initialisation
+ *                its contents need no initialisation, and calls whose kernels may overlap
+ *                need one each
  * Errors as for gdla_cache_append, plus GDLA_ERR_UNSUPPORTED for sinks > GDLA_MAX_SINKS and
  * GDLA_ERR_WORKSPACE.
  */
