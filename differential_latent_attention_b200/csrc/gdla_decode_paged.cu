@@ -327,8 +327,11 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
     // e4m3: O is held in units of vs_unit, the V scale of some page, and the probabilities take the ratio of
     // their own page's to it, so that the products add straight onto O. Within 2^-8 .. 2^8 of it an f16
     // probability loses nothing that its own rounding does not (at most 2^-17 of the page's scale); a page
-    // further off changes the unit.
-    float vs_unit = 1.f, vs_inv = 1.f;
+    // further off changes the unit, down to 2^-90 of the largest one so far at most: O, under 2^37 of those, stays
+    // finite, and a page whose scale is smaller yet (one of zeros has 2^-110) is lost beside them. The first unit,
+    // 2^-12, takes pages that all have the least scale. Held are 1 / unit and the least unit.
+    constexpr float kUnitDrop = 8.077935669463161e-28f;  // 2^-90
+    float vs_inv = 4096.f, vs_floor = kUnitDrop / 4096.f;
     for (int n = 0; n < mine; ++n) {
         const int st = n % STAGES;
         const uint8_t *kb = ring + st * C::STAGE, *vb = kb + C::K_BYTES;
@@ -412,12 +415,12 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
             if constexpr (E4M3) {
                 float ratio = a.w * vs_inv;
                 if (!(ratio >= 0.00390625f && ratio <= 256.f) && a.w >= 1e-37f && a.w <= 1e37f) {
-                    const float f = vs_unit / a.w;
+                    const float unit = fmaxf(a.w, vs_floor), f = 1.f / (unit * vs_inv);
 #pragma unroll
                     for (int mt = 0; mt < DV / 16; ++mt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[mt][e] = o[mt][e] == 0.f ? 0.f : o[mt][e] * f;
-                    vs_unit = a.w, vs_inv = 1.f / a.w, ratio = 1.f;
+                        for (int e = 0; e < 4; ++e) o[mt][e] *= f;
+                    vs_inv = 1.f / unit, vs_floor = fmaxf(vs_floor, unit * kUnitDrop), ratio = a.w * vs_inv;
                 }
                 p0 *= ratio, p1 *= ratio, p2 *= ratio, p3 *= ratio;
             }
@@ -525,7 +528,7 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
         M1 = fmaxf(M1, ml[(w * 8 + 2 * c + 1) * 2]);
     }
     float w0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M0), w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M1);
-    if constexpr (E4M3) w0 *= vs_unit, w1 *= vs_unit;
+    if constexpr (E4M3) w0 /= vs_inv, w1 /= vs_inv;
 #pragma unroll
     for (int mt = 0; mt < DV / 16; ++mt) {
         float *dst = red + (warp * HEADS + 2 * c) * RED_ROW + 16 * mt + 2 * g8;

@@ -163,6 +163,35 @@ def test_scales_of_every_size():
         check_decode(got, plain_decode(**d, pool=pool, table=table, page=page, lens=lens, window=page), exps)
 
 
+def test_pages_of_zeros_between_large_ones():
+    """A page of zeros has the least scale, 2^-110; what the pages around it gave stays finite and as it was."""
+    page, heads = 16, 2
+    for exps in ([32, None, 32, 30, None, None, 31], [None, -7, None, -7, -6, None, -7], [None] * 7, [-110] * 7):
+        lens = [7 * page, 2 * page]
+        d, pool, table = _case(lens, heads, page, "e4m3", 565)
+        for b in range(2):
+            for j, e in enumerate(exps):
+                if j < table.shape[1] and int(table[b, j]) >= 0:
+                    pool["v_scale"][int(table[b, j])] = 2.0 ** (-110 if e is None else e)
+                    if e is None:
+                        pool["v_pages"][int(table[b, j])] = 0
+        for window in (0, page):
+            got = _run(d, pool, table, lens, window=window)
+            check_decode(got, plain_decode(**d, pool=pool, table=table, page=page, lens=lens, window=window), (exps, window))
+    # one warp takes many blocks on both sides of the zeros: sums of 2^16 units and more
+    for exp in (0, 40):
+        lens = [4096] * 640
+        d, pool, table = decode_inputs(640, 1, 566), new_pool(6, 1, 128, "e4m3", 566), torch.zeros((640, 32), dtype=torch.int32, device="cuda")
+        table[:] = torch.arange(32, device="cuda") % 5
+        table[:, 20] = 5
+        pool["v_pages"].fill_(448.0)
+        pool["v_scale"][:] = 2.0 ** exp
+        pool["v_pages"][5], pool["v_scale"][5] = 0, 2.0 ** -110
+        got = _run(d, pool, table, lens)
+        some = {k: x[:4] for k, x in d.items()}
+        check_decode(got[:4], plain_decode(**some, pool=pool, table=table, page=128, lens=lens[:4]), exp)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_sharp_and_growing_scores(kind):
     """Scores that grow along the sequence (the running maximum moves all the time) and one key that takes all."""
