@@ -66,10 +66,13 @@ __device__ __forceinline__ AppendUnit append_unit(const AppendPlan &p, int u) {
     AppendUnit a{};
     const int b = append_sequence<STEP>(p, u);
     const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1], len = p.seqlens_k[b];
-    const int n = c1 - c0, before = len - n, P = p.page_size;
-    if (c0 < 0 || n < 1 || c1 > p.num_tokens || before < 0 || len > p.max_pages * static_cast<long long>(P)) return a;
-    const int first = (c0 >> p.page_shift) + 2 * b, j = (before >> p.page_shift) + (u - first);
-    if (u < first || j > (len - 1) >> p.page_shift) return a;
+    const int P = p.page_size;
+    if (c0 < 0 || c1 <= c0 || c1 > p.num_tokens || len > p.max_pages * static_cast<long long>(P)) return a;
+    const int n = c1 - c0;
+    if (len < n) return a;  // (compared, not subtracted: a length of -2^31 would come back positive)
+    const int before = len - n, first = (c0 >> p.page_shift) + 2 * b, page0 = before >> p.page_shift;
+    if (u < first || u - first > ((len - 1) >> p.page_shift) - page0) return a;
+    const int j = page0 + (u - first);
     a.fits = true;
     a.page = p.block_table[static_cast<size_t>(b) * p.max_pages + j];
     a.pos0 = j << p.page_shift;

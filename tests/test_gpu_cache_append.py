@@ -250,6 +250,12 @@ def test_what_does_not_fit_is_skipped(kind, n):
     _run(c, pool, lens=_i32([10 ** 6] * 4))
     _run(c, pool, cu=_i32([0, 10 ** 6, 10 ** 6 + 1, 10 ** 6 + 2, 10 ** 6 + 3]))
     _run(c, pool, cu=_i32([-5, -4, -3, -2, -1]))
+    least, most = -2 ** 31, 2 ** 31 - 1             # differences of these leave 32 bits
+    _run(c, pool, lens=_i32([least, least + n - 1, least + n, -1]))
+    _run(c, pool, lens=_i32([most, most - 1, most - n, most]))
+    _run(c, pool, cu=_i32([most, least, most, least, most]))
+    _run(c, pool, cu=_i32([least, most, least, most, least]))
+    _run(c, pool, cu=_i32([least] * 5))
     for name in ("k_pages", "v_pages"):
         assert torch.equal(_raw(pool[name]), _raw(c["pool"][name]))
 
