@@ -39,17 +39,16 @@ struct AppendUnit {
     int slot0, slot1;    // slots that the call fills
     int tok0;            // token of slot0
 };
-// The sequence of unit u, the last one whose first unit is <= u; the whole warp calls. A step's
-// sequences bring about one token each, so STEP looks first where u would be if all did. Otherwise each round the
-// lanes try 32 places of what is left: 1,024 sequences take two dependent loads.
-template <bool STEP>
-__device__ __forceinline__ int append_sequence(const AppendPlan &p, int u) {
+// The sequence of unit u, the last one whose first unit is <= u; the whole warp calls. The lanes look first at the
+// 32 sequences around where u would be if all brought equally many tokens (`per_unit` sequences a unit), which finds
+// steps and up to 32 sequences at once. Otherwise each round tries 32 places of what is left: 1,024 sequences take
+// two more dependent loads.
+__device__ __forceinline__ int append_sequence(const AppendPlan &p, int u, float per_unit) {
     const auto first = [&](int b) { return (p.cu_new[b] >> p.page_shift) + 2 * b; };
-    if (STEP) {
-        const int b = min(static_cast<int>((static_cast<long long>(u) << p.page_shift) / (2 * p.page_size + 1)), p.batch - 1);
-        if (first(b) <= u && u < first(b + 1)) return b;
-    }
     const int lane = threadIdx.x & 31;
+    const int near = max(0, min(static_cast<int>(static_cast<float>(u) * per_unit) - 16, p.batch - 32));
+    const unsigned seen = __ballot_sync(0xffffffffu, near + lane < p.batch && first(near + lane) <= u);
+    if ((near == 0 || (seen & 1u)) && (near + 32 >= p.batch || !(seen >> 31))) return near + max(__popc(seen) - 1, 0);
     int b = 0, left = p.batch;  // it is one of b .. b + left - 1
     while (left > 1) {
         const int step = (left + 31) / 32, mine = b + lane * step;
@@ -61,10 +60,9 @@ __device__ __forceinline__ int append_sequence(const AppendPlan &p, int u) {
     }
     return b;
 }
-template <bool STEP>
-__device__ __forceinline__ AppendUnit append_unit(const AppendPlan &p, int u) {
+__device__ __forceinline__ AppendUnit append_unit(const AppendPlan &p, int u, float per_unit) {
     AppendUnit a{};
-    const int b = append_sequence<STEP>(p, u);
+    const int b = append_sequence(p, u, per_unit);
     const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1], len = p.seqlens_k[b];
     const int P = p.page_size;
     if (c0 < 0 || c1 <= c0 || c1 > p.num_tokens || len > p.max_pages * static_cast<long long>(P)) return a;
@@ -185,20 +183,112 @@ __device__ __forceinline__ int block_exponent(uint32_t amax_bits, bool goes_on, 
     return e;
 }
 
-// Whole pages: one CTA per (unit, HEADS heads). A page and head's new values stay in registers
+// Few rows (a decode step): one warp per head, every row in its registers; lanes 0..15 hold a row's K content,
+// 16..31 its V, and lane i pair i of the rotary part as well.
+constexpr int kFewRows = 4;
+template <bool E4M3>
+__device__ __forceinline__ void append_few(const AppendPlan &p, const AppendUnit &a, int h0, int h1) {
+    const int n = a.slot1 - a.slot0, lane = threadIdx.x & 31;
+    const bool is_k = lane < 16;
+    float lo[kFewRows], hi[kFewRows];  // rotary pair `lane`
+    float rope_max = 0.f;
+#pragma unroll
+    for (int r = 0; r < kFewRows; ++r) {
+        lo[r] = hi[r] = 0.f;
+        if (r < n) {
+            const __nv_bfloat16 *rope = p.k_rope + static_cast<size_t>(a.tok0 + r) * p.rope_token + lane;
+            lo[r] = __bfloat162float(rope[0]);
+            hi[r] = __bfloat162float(rope[32]);
+        }
+    }
+    for (int h = h0 + (threadIdx.x >> 5); h < h1; h += 8) {
+        const __nv_bfloat16 *src = is_k ? p.k_nope + static_cast<size_t>(a.tok0) * p.nope_token + h * p.nope_head + 8 * lane
+                                        : p.v + static_cast<size_t>(a.tok0) * p.v_token + h * p.v_head + 8 * (lane - 16);
+        const long long step = is_k ? p.nope_token : p.v_token;
+        uint4 x[kFewRows];  // eight values of K's content or V
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r)
+            x[r] = r < n ? __ldg(reinterpret_cast<const uint4 *>(src + r * step)) : make_uint4(0u, 0u, 0u, 0u);
+        if (!in_pool(p, a.page)) return;
+        const size_t blk = static_cast<size_t>(a.page) * p.hkv + h, slot = (blk << p.page_shift) + a.slot0;
+        const bool goes_on = E4M3 && a.slot0 > 0;
+        const float k_had = goes_on ? p.k_scale[blk] : 0.f, v_had = goes_on ? p.v_scale[blk] : 0.f;
+        if (h < h0 + 8) {  // the warp's first head: turn the keys while the rows are under way
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) {
+                if (r < n && p.rotate) {
+                    double c, s;
+                    rotary_angle(a.pos0 + a.slot0 + r, lane, c, s);
+                    const double y = lo[r], z = hi[r];
+                    lo[r] = static_cast<float>(y * c - z * s);
+                    hi[r] = static_cast<float>(y * s + z * c);
+                }
+                if (E4M3) rope_max = fmaxf(rope_max, fmaxf(finite_abs(lo[r]), finite_abs(hi[r])));
+            }
+        }
+        if constexpr (!E4M3) {
+            __nv_bfloat16 *kd = static_cast<__nv_bfloat16 *>(p.k_pages) + slot * 192;
+            __nv_bfloat16 *vd = static_cast<__nv_bfloat16 *>(p.v_pages) + slot * 128;
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) {
+                if (r < n) {
+                    *reinterpret_cast<uint4 *>(is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16)) = x[r];
+                    kd[r * 192 + 128 + lane] = __float2bfloat16_rn(lo[r]);
+                    kd[r * 192 + 160 + lane] = __float2bfloat16_rn(hi[r]);
+                }
+            }
+        } else {
+            uint32_t mine = 0u;
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) {
+                const uint32_t raw = max_bits(x[r]);
+                mine = max(mine, raw < kInfBits ? raw : finite_max_bits(x[r]));
+            }
+            const uint32_t km = __reduce_max_sync(0xffffffffu, max(is_k ? mine : 0u, __float_as_uint(rope_max)));
+            const uint32_t vm = __reduce_max_sync(0xffffffffu, is_k ? 0u : mine);
+            float k_shrink, v_shrink;
+            const int ke = block_exponent(km, goes_on, k_had, k_shrink);
+            const int ve = block_exponent(vm, goes_on, v_had, v_shrink);
+            uint8_t *kd = static_cast<uint8_t *>(p.k_pages) + slot * 192;
+            uint8_t *vd = static_cast<uint8_t *>(p.v_pages) + slot * 128;
+            if (k_shrink < 1.f) shrink_codes(kd - a.slot0 * 192, a.slot0 * 192, k_shrink, lane, 32);
+            if (v_shrink < 1.f) shrink_codes(vd - a.slot0 * 128, a.slot0 * 128, v_shrink, lane, 32);
+            const float ki = power_of_two(-ke), vi = power_of_two(-ve);
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) {
+                if (r < n) {
+                    uint8_t *dst = is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16);
+                    *reinterpret_cast<uint2 *>(dst) = to_e4m3<false>(x[r], is_k ? ki : vi);
+                    const uint32_t two = pair_e4m3<false>(lo[r], hi[r], ki);
+                    kd[r * 192 + 128 + lane] = static_cast<uint8_t>(two);
+                    kd[r * 192 + 160 + lane] = static_cast<uint8_t>(two >> 8);
+                }
+            }
+            if (lane == 0 && (k_had != power_of_two(ke) || v_had != power_of_two(ve)))
+                p.k_scale[blk] = power_of_two(ke), p.v_scale[blk] = power_of_two(ve);
+        }
+    }
+}
+
+// One CTA per (unit, heads_per_cta heads); a unit of few rows goes to its warps, one head each. Otherwise a page and head's new values stay in registers
 // between the search for the largest and the writing, so each input is read once; the turned rotary
 // key is shared by the CTA's heads. NI = page_size / 16: 16-byte pieces of K's content (and of
 // V) per thread.
 template <bool E4M3, int NI>
 __global__ void __launch_bounds__(256, NI <= 4 ? 3 : 2)
-gdla_cache_append_kernel(const __grid_constant__ AppendPlan p) {
+gdla_cache_append_kernel(const __grid_constant__ AppendPlan p, float per_unit) {
     constexpr int NR = NI <= 4 ? 1 : NI / 4;  // rotary pieces (8 pairs) per thread
     __shared__ uint32_t red[2][2][8];
     const int groups = (p.hkv + p.heads_per_cta - 1) / p.heads_per_cta;
     const int u = blockIdx.x / groups;
-    const AppendUnit a = append_unit<false>(p, u);
+    const AppendUnit a = append_unit(p, u, per_unit);
     if (!a.fits) return;
     const int n = a.slot1 - a.slot0, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int h0 = (blockIdx.x - u * groups) * p.heads_per_cta, h1 = min(p.hkv, h0 + p.heads_per_cta);
+    if (n <= kFewRows) {
+        append_few<E4M3>(p, a, h0, h1);
+        return;
+    }
     const int row = t >> 4, col = t & 15;     // pieces (row + 16 i, col)
     const int rrow = t >> 2, rq = t & 3;      // rotary pieces (rrow + 64 i, rq)
     RopePart rope[NR];
@@ -212,7 +302,6 @@ gdla_cache_append_kernel(const __grid_constant__ AppendPlan p) {
         }
     }
     if (!in_pool(p, a.page)) return;
-    const int h0 = (blockIdx.x - u * groups) * p.heads_per_cta, h1 = min(p.hkv, h0 + p.heads_per_cta);
     const size_t tok = static_cast<size_t>(a.tok0 + row);
     const __nv_bfloat16 *k_src = p.k_nope + tok * p.nope_token + h0 * p.nope_head + 8 * col;
     const __nv_bfloat16 *v_src = p.v + tok * p.v_token + h0 * p.v_head + 8 * col;
@@ -311,122 +400,40 @@ gdla_cache_append_kernel(const __grid_constant__ AppendPlan p) {
     }
 }
 
-// Few tokens per sequence (a decode step): one warp per (unit, head), row by row; lanes 0..15 hold
-// a row's K content, 16..31 its V, and lane i pair i of the rotary part as well.
 template <bool E4M3>
-__global__ void __launch_bounds__(128)
-gdla_cache_append_step_kernel(const __grid_constant__ AppendPlan p, int units) {
-    const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int u = w / p.hkv, h = w - u * p.hkv;
-    if (u >= units) return;
-    const AppendUnit a = append_unit<true>(p, u);
-    if (!a.fits) return;
-    const int n = a.slot1 - a.slot0;
-    const bool is_k = lane < 16;
-    const __nv_bfloat16 *src = is_k ? p.k_nope + static_cast<size_t>(a.tok0) * p.nope_token + h * p.nope_head + 8 * lane
-                                    : p.v + static_cast<size_t>(a.tok0) * p.v_token + h * p.v_head + 8 * (lane - 16);
-    const long long step = is_k ? p.nope_token : p.v_token;
-    struct Row {
-        uint4 x;       // this lane's eight values of K's content or V
-        float lo, hi;  // its rotary pair
-    };
-    const auto fetch = [&](int r) {
-        Row y;
-        y.x = __ldg(reinterpret_cast<const uint4 *>(src + r * step));
-        const __nv_bfloat16 *rope = p.k_rope + static_cast<size_t>(a.tok0 + r) * p.rope_token + lane;
-        y.lo = __bfloat162float(rope[0]);
-        y.hi = __bfloat162float(rope[32]);
-        if (p.rotate) {
-            double c, s;
-            rotary_angle(a.pos0 + a.slot0 + r, lane, c, s);
-            const double lo = y.lo, hi = y.hi;
-            y.lo = static_cast<float>(lo * c - hi * s);
-            y.hi = static_cast<float>(lo * s + hi * c);
-        }
-        return y;
-    };
-    Row row = fetch(n - 1);  // the last row (of a step: the only one) is under way while the page's entry comes
-    if (!in_pool(p, a.page)) return;
-    const size_t blk = static_cast<size_t>(a.page) * p.hkv + h, slot = (blk << p.page_shift) + a.slot0;
-    if constexpr (!E4M3) {
-        __nv_bfloat16 *kd = static_cast<__nv_bfloat16 *>(p.k_pages) + slot * 192;
-        __nv_bfloat16 *vd = static_cast<__nv_bfloat16 *>(p.v_pages) + slot * 128;
-        for (int r = n - 1; r >= 0; --r) {
-            if (r < n - 1) row = fetch(r);
-            *reinterpret_cast<uint4 *>(is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16)) = row.x;
-            kd[r * 192 + 128 + lane] = __float2bfloat16_rn(row.lo);
-            kd[r * 192 + 160 + lane] = __float2bfloat16_rn(row.hi);
-        }
-    } else {
-        const bool goes_on = a.slot0 > 0;
-        const float k_had = goes_on ? p.k_scale[blk] : 0.f, v_had = goes_on ? p.v_scale[blk] : 0.f;
-        uint32_t km = 0u, vm = 0u;
-        const auto largest = [&](const Row &y) {
-            const uint32_t raw = max_bits(y.x), m = raw < kInfBits ? raw : finite_max_bits(y.x);
-            if (is_k)
-                km = max(km, m);
-            else
-                vm = max(vm, m);
-            km = max(km, __float_as_uint(fmaxf(finite_abs(y.lo), finite_abs(y.hi))));
-        };
-        largest(row);  // it stays for the writing: with one row nothing is read twice
-        for (int r = 0; r < n - 1; ++r) largest(fetch(r));
-        km = __reduce_max_sync(0xffffffffu, km);
-        vm = __reduce_max_sync(0xffffffffu, vm);
-        float k_shrink, v_shrink;
-        const int ke = block_exponent(km, goes_on, k_had, k_shrink);
-        const int ve = block_exponent(vm, goes_on, v_had, v_shrink);
-        uint8_t *kd = static_cast<uint8_t *>(p.k_pages) + slot * 192;
-        uint8_t *vd = static_cast<uint8_t *>(p.v_pages) + slot * 128;
-        if (k_shrink < 1.f) shrink_codes(kd - a.slot0 * 192, a.slot0 * 192, k_shrink, lane, 32);
-        if (v_shrink < 1.f) shrink_codes(vd - a.slot0 * 128, a.slot0 * 128, v_shrink, lane, 32);
-        const float ki = power_of_two(-ke), vi = power_of_two(-ve);
-        for (int r = n - 1; r >= 0; --r) {
-            if (r < n - 1) row = fetch(r);
-            uint8_t *dst = is_k ? kd + r * 192 + 8 * lane : vd + r * 128 + 8 * (lane - 16);
-            *reinterpret_cast<uint2 *>(dst) = to_e4m3<false>(row.x, is_k ? ki : vi);
-            const uint32_t two = pair_e4m3<false>(row.lo, row.hi, ki);
-            kd[r * 192 + 128 + lane] = static_cast<uint8_t>(two);
-            kd[r * 192 + 160 + lane] = static_cast<uint8_t>(two >> 8);
-        }
-        if (lane == 0 && (k_had != power_of_two(ke) || v_had != power_of_two(ve)))
-            p.k_scale[blk] = power_of_two(ke), p.v_scale[blk] = power_of_two(ve);
-    }
-}
-
-template <bool E4M3>
-static void launch_append_pages(const AppendPlan &p, unsigned grid, cudaStream_t stream) {
+static void launch_append_pages(const AppendPlan &p, float per_unit, unsigned grid, cudaStream_t stream) {
     switch (p.page_size) {
-        case 16: gdla_cache_append_kernel<E4M3, 1><<<grid, 256, 0, stream>>>(p); break;
-        case 32: gdla_cache_append_kernel<E4M3, 2><<<grid, 256, 0, stream>>>(p); break;
-        case 64: gdla_cache_append_kernel<E4M3, 4><<<grid, 256, 0, stream>>>(p); break;
-        default: gdla_cache_append_kernel<E4M3, 8><<<grid, 256, 0, stream>>>(p); break;
+        case 16: gdla_cache_append_kernel<E4M3, 1><<<grid, 256, 0, stream>>>(p, per_unit); break;
+        case 32: gdla_cache_append_kernel<E4M3, 2><<<grid, 256, 0, stream>>>(p, per_unit); break;
+        case 64: gdla_cache_append_kernel<E4M3, 4><<<grid, 256, 0, stream>>>(p, per_unit); break;
+        default: gdla_cache_append_kernel<E4M3, 8><<<grid, 256, 0, stream>>>(p, per_unit); break;
     }
 }
 
 cudaError_t launch_cache_append(const AppendPlan &plan, bool e4m3, cudaStream_t stream) {
     AppendPlan p = plan;
     const long long units = p.num_tokens / p.page_size + 2ll * p.batch;
-    if (p.num_tokens <= 2ll * p.batch) {
-        const unsigned grid = static_cast<unsigned>((units * p.hkv + 3) / 4);
-        if (e4m3)
-            gdla_cache_append_step_kernel<true><<<grid, 128, 0, stream>>>(p, static_cast<int>(units));
-        else
-            gdla_cache_append_step_kernel<false><<<grid, 128, 0, stream>>>(p, static_cast<int>(units));
-        return cudaPeekAtLastError();
-    }
-    // Heads of a CTA: 128 rows' worth (fewer and the search and the turned keys weigh more, us at 1, 2, 4, 8 heads: 13 chunks
-    // of 400 tokens, 5 heads, bf16 pages of 16: 13.3, 11.2, 8.8, 7.6; 8,000 tokens, 16 heads, e4m3 pages of 32: 40, 32, 30, 33),
-    // four at least in large calls (32,600 tokens, e4m3 pages of 64: 119, 91, 82, 83), as long as every SM gets a CTA.
+    // Heads of a CTA. Prompts: 128 rows' worth (fewer and the search and the turned keys weigh more, us at 1, 2, 4, 8
+    // heads: 13 chunks of 400 tokens, 5 heads, bf16 pages of 16: 13.3, 11.2, 8.8, 7.6; 8,000 tokens, 16 heads, e4m3 pages
+    // of 32: 40, 32, 30, 33), four at least in large calls (32,600 tokens, e4m3 pages of 64: 119, 91, 82, 83).
+    // Steps of one token: a head per warp or, once those CTAs would not all run at once, two (us at 4, 8, 16 heads, bf16
+    // pages of 64: 64 sequences 4.0, 3.7, 4.0; 256: 9.2, 6.8, 5.2). Between them four heads, or eight for many
+    // short ones (us at 2, 4, 8 heads, e4m3 pages of 64: 63 steps beside a chunk of 65 9.2, 8.5, 11.5; 255 beside
+    // 1,024 20.8, 20.8, 23.4; 64 x 4 tokens 8.7, 6.3, 6.8). In each as long as every SM gets a CTA.
     const long long pairs = units * p.hkv;
     long long heads = 128 / p.page_size;
-    if (pairs >= 32ll * kPlanSms) heads = std::max(heads, 4ll);
+    if (p.num_tokens <= p.batch)
+        heads = std::max(8ll, pairs / (3 * kPlanSms));
+    else if (pairs >= 32ll * kPlanSms || p.num_tokens <= 16ll * p.batch)
+        heads = std::max(heads, 4ll);
+    if (p.num_tokens > p.batch && p.num_tokens <= 4ll * p.batch) heads = std::max(heads, std::min(8ll, pairs / (6 * kPlanSms)));
     p.heads_per_cta = static_cast<int>(std::max(1ll, std::min(heads, std::min<long long>(p.hkv, pairs / kPlanSms))));
+    const float per_unit = static_cast<float>(p.batch) / static_cast<float>(units);
     const unsigned grid = static_cast<unsigned>(units * ((p.hkv + p.heads_per_cta - 1) / p.heads_per_cta));
     if (e4m3)
-        launch_append_pages<true>(p, grid, stream);
+        launch_append_pages<true>(p, per_unit, grid, stream);
     else
-        launch_append_pages<false>(p, grid, stream);
+        launch_append_pages<false>(p, per_unit, grid, stream);
     return cudaPeekAtLastError();
 }
 

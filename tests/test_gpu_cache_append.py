@@ -260,6 +260,18 @@ def test_what_does_not_fit_is_skipped(kind, n):
         assert torch.equal(_raw(pool[name]), _raw(c["pool"][name]))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_steps_beside_chunks(kind, page):
+    """Units of one to five rows (also a chunk's last page) beside whole pages, and sequences that bring nothing for long
+    stretches, so that the search for a unit's sequence starts far from it."""
+    new = [1] * 20 + [page + 3, 3, 4, 5, 6, 2 * page + 4, 2 * page + 5, 1]
+    old = [(7 * i) % (2 * page) for i in range(20)] + [0, page - 2, page - 4, 11, page - 1, 0, page - 3, 0]
+    _check(new, [n + o for n, o in zip(new, old)], 3, page, kind, 1101)
+    new = [0] * 90 + [3 * page + 1] + [0] * 60 + [1, 2, 0, page] + [0] * 50 + [1]
+    _check(new, [n + (5 * i) % page for i, n in enumerate(new)], 9, page, kind, 1102)
+
+
 def test_no_tokens():
     c = _case([0], [5], 2, 16, "bf16", 71)
     pool = _clone(c["pool"])
