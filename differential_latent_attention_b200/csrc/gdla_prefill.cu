@@ -365,6 +365,9 @@ __device__ __forceinline__ void epi_backward(uint32_t o_addr, float l_run, float
 
 }  // namespace pf
 
+// Bits 0 .. c - 1 of a word (none for c <= 0, all for c >= 32).
+__device__ __forceinline__ uint32_t bits_below(int c) { return c >= 32 ? 0xFFFFFFFFu : (1u << max(c, 0)) - 1u; }
+
 template <class C, class Plan>
 __global__ void __launch_bounds__(C::NUM_THREADS, 1)
 gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_constant__ CUtensorMap tm_qn,
@@ -740,11 +743,14 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
                     // visible columns: keys lo_t..t of this row
                     const int c_lo = lo_t - u0, c_hi = t - u0;
                     if constexpr (C::SINK) {
-                        // and the sinks, whose columns come first
+                        // and the sinks, whose columns come first: as bits, one test a column instead of three compares
                         const int c_sink = plan.sinks - k * BN;
 #pragma unroll
-                        for (int i = 0; i < BN; ++i)
-                            s[i] = (i <= c_hi && (i >= c_lo || i < c_sink)) ? s[i] : -INFINITY;
+                        for (int w32 = 0; w32 < BN; w32 += 32) {
+                            const uint32_t seen = bits_below(c_hi + 1 - w32) & (~bits_below(c_lo - w32) | bits_below(c_sink - w32));
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) s[w32 + i] = (seen >> i & 1u) ? s[w32 + i] : -INFINITY;
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < BN; ++i) s[i] = (i >= c_lo && i <= c_hi) ? s[i] : -INFINITY;
