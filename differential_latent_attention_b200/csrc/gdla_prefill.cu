@@ -742,18 +742,14 @@ gdla_prefill_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
                 if (need_mask) {
                     // visible columns: keys lo_t..t of this row
                     const int c_lo = lo_t - u0, c_hi = t - u0;
-                    if constexpr (C::SINK) {
-                        // and the sinks, whose columns come first: as bits, one test a column instead of three compares
-                        const int c_sink = plan.sinks - k * BN;
+                    // (with sinks those too, whose columns come first), as bits: one test a column
 #pragma unroll
-                        for (int w32 = 0; w32 < BN; w32 += 32) {
-                            const uint32_t seen = bits_below(c_hi + 1 - w32) & (~bits_below(c_lo - w32) | bits_below(c_sink - w32));
+                    for (int w32 = 0; w32 < BN; w32 += 32) {
+                        uint32_t unseen = bits_below(c_lo - w32);
+                        if constexpr (C::SINK) unseen &= ~bits_below(plan.sinks - k * BN - w32);
+                        const uint32_t seen = bits_below(c_hi + 1 - w32) & ~unseen;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) s[w32 + i] = (seen >> i & 1u) ? s[w32 + i] : -INFINITY;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < BN; ++i) s[i] = (i >= c_lo && i <= c_hi) ? s[i] : -INFINITY;
+                        for (int i = 0; i < 32; ++i) s[w32 + i] = (seen >> i & 1u) ? s[w32 + i] : -INFINITY;
                     }
                 }
                 float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
