@@ -48,7 +48,7 @@ __device__ __forceinline__ int dim_of(int place) {
     const int mt = place >> 4, g8 = (place >> 1) & 7, e = place & 1;
     return E4M3 ? 16 * g8 + 2 * mt + e : 16 * mt + g8 + 8 * e;
 }
-constexpr float kTrail = 4.f;  // a probability is at most 2^4; with a V scale's ratio of 2^8 it stays in f16
+constexpr float kTrail = 4.f;  // a probability is at most 2^4: with the largest ratio and the bias 2^15, which f16 holds
 constexpr float kScoreLog2 = 0.07216878364870322f * 1.4426950408889634f;  // log2(e) / sqrt(192)
 
 // Warps per CTA: 4, or 8 for few items, or 2 for many of few keys each (then a warp's own start and end weigh more
@@ -324,14 +324,17 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
     // Running maxima of heads 2c, 2c+1 (log2 units) and their sums. The maxima may trail the true ones by
     // kTrail: then a block costs one vote, and no reduction over the keys and no rescaling.
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    // e4m3: O is held in units of vs_unit, the V scale of some page, and the probabilities take the ratio of
-    // their own page's to it, so that the products add straight onto O. Within 2^-8 .. 2^8 of it an f16
-    // probability loses nothing that its own rounding does not (at most 2^-17 of the page's scale); a page
-    // further off changes the unit, down to 2^-90 of the largest one so far at most: O, under 2^37 of those, stays
-    // finite, and a page whose scale is smaller yet (one of zeros has 2^-110) is lost beside them. The first unit,
-    // 2^-12, takes pages that all have the least scale. Held are 1 / unit and the least unit.
-    constexpr float kUnitDrop = 8.077935669463161e-28f;  // 2^-90
-    float vs_inv = 4096.f, vs_floor = kUnitDrop / 4096.f;
+    // e4m3: O is held in units of 1 / kBias of some page's V scale, the first page's to begin with, and the probabilities
+    // take kBias and the ratio of their own page's scale to that one, so that the products add straight onto O. Ratios
+    // from 2^-4 to 2^2 leave an f16 probability its 11 bits down to 2^-19 of the running maximum, or further, and a step
+    // of 2^-29 under that (p <= 2^kTrail, so 2^15 at most); a page further off changes the unit. Without the bias, and with
+    // ratios from 2^-8 on, a key that took nearly all the weight left the others 2^-17 of it as step: 1e-3 to
+    // 2e-2 of the output where its own value was small. The unit goes down to 2^-75 of the largest one so far at most: O,
+    // under 2^51 of those, stays finite, and a page whose scale is smaller yet (one of zeros has 2^-110) is lost beside
+    // them. Held are 1 / unit (0: no page yet) and the least unit.
+    constexpr float kBias = 512.f, kRatioMin = kBias / 16.f, kRatioMax = kBias * 4.f;
+    constexpr float kUnitDrop = 2.6469779601696886e-23f;  // 2^-75
+    float vs_inv = 0.f, vs_floor = 0.f;
     for (int n = 0; n < mine; ++n) {
         const int st = n % STAGES;
         const uint8_t *kb = ring + st * C::STAGE, *vb = kb + C::K_BYTES;
@@ -414,13 +417,14 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
             l1 += p1 + p3;
             if constexpr (E4M3) {
                 float ratio = a.w * vs_inv;
-                if (!(ratio >= 0.00390625f && ratio <= 256.f) && a.w >= 1e-37f && a.w <= 1e37f) {
-                    const float unit = fmaxf(a.w, vs_floor), f = 1.f / (unit * vs_inv);
+                const float size = fabsf(a.w);
+                if (!(fabsf(ratio) >= kRatioMin && fabsf(ratio) <= kRatioMax) && size >= 1e-35f) {
+                    const float unit = fmaxf(size, vs_floor), inv = kBias / unit, f = vs_inv > 0.f ? inv / vs_inv : 1.f;
 #pragma unroll
                     for (int mt = 0; mt < DV / 16; ++mt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[mt][e] *= f;
-                    vs_inv = 1.f / unit, vs_floor = fmaxf(vs_floor, unit * kUnitDrop), ratio = a.w * vs_inv;
+                    vs_inv = inv, vs_floor = fmaxf(vs_floor, unit * kUnitDrop), ratio = a.w * inv;
                 }
                 p0 *= ratio, p1 *= ratio, p2 *= ratio, p3 *= ratio;
             }
@@ -528,7 +532,9 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
         M1 = fmaxf(M1, ml[(w * 8 + 2 * c + 1) * 2]);
     }
     float w0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M0), w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M1);
-    if constexpr (E4M3) w0 /= vs_inv, w1 /= vs_inv;
+    if constexpr (E4M3) {
+        if (vs_inv > 0.f) w0 /= vs_inv, w1 /= vs_inv;
+    }
 #pragma unroll
     for (int mt = 0; mt < DV / 16; ++mt) {
         float *dst = red + (warp * HEADS + 2 * c) * RED_ROW + 16 * mt + 2 * g8;
