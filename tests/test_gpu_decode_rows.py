@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from _paged import BF16_HALF, GROUP, decode_inputs, new_pool, plain_decode
-from test_gpu_decode_paged import _case, _run
+from test_gpu_decode_paged import EDGES, _case, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -28,6 +28,30 @@ def check_rows(got, ref, what):
     assert float(rms.max()) <= ROWS_RMS, (what, float(rms.max()))
     top = b.abs().amax(-1, keepdim=True)
     assert bool(((a - b).abs() <= BF16_HALF * b.abs() + 1e-2 * top).all()), what
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_edge_lengths(kind, page):
+    d, pool, table = _case(EDGES, 2, page, kind, 700 + page)
+    check_rows(_run(d, pool, table, EDGES), plain_decode(**d, pool=pool, table=table, page=page, lens=EDGES), (kind, page))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window, sinks", [(1, 0), (1, 1), (16, 4), (100, 17), (128, 4), (129, 128), (1000, 5), (5000, 64)])
+def test_windows_and_sinks(kind, window, sinks):
+    d, pool, table = _case(EDGES, 3, 16, kind, 800 + window)
+    kw = dict(window=window, sinks=sinks)
+    check_rows(_run(d, pool, table, EDGES, **kw), plain_decode(**d, pool=pool, table=table, page=16, lens=EDGES, **kw), (kind, kw))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window, sinks", [(0, 0), (130, 9)])
+def test_turned_queries(kind, window, sinks):
+    lens = [1, 70, 513, 4001]
+    d, pool, table = _case(lens, 2, 64, kind, 900)
+    kw = dict(window=window, sinks=sinks, rotate=True)
+    check_rows(_run(d, pool, table, lens, **kw), plain_decode(**d, pool=pool, table=table, page=64, lens=lens, **kw), (kind, kw))
 
 
 @pytest.mark.parametrize("lens, heads", [([1, 17, 300, 2049], 2), ([4096], 16), ([20011, 77], 1), ([300] * 320, 2)])
