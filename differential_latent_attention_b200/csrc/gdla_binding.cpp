@@ -7,6 +7,7 @@
 // this module has nothing of it linked in; PyTorch gives memory, the current stream and the errors' types.
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -143,6 +144,22 @@ c10::cuda::CUDAStream launch_stream(PyObject *given, int64_t dev) {
     return c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(ptr), static_cast<c10::DeviceIndex>(dev));
 }
 
+// Memory that a call makes itself, for kernels on stream `on`. The allocator hands out a freed block as soon as its own
+// stream's order allows, so memory of the current stream may still be in use there when another stream writes it: it
+// comes from the launch stream's blocks. The caller has it on the current stream, which is made known to the allocator for
+// the day it is freed.
+at::Tensor empty_for(const c10::cuda::CUDAStream &on, at::IntArrayRef shape, const at::TensorOptions &options) {
+    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(on.device_index());
+    if (now.stream() == on.stream()) return at::empty(shape, options);
+    at::Tensor t;
+    {
+        const c10::cuda::CUDAStreamGuard guard(on);
+        t = at::empty(shape, options);
+    }
+    t.record_stream(now);
+    return t;
+}
+
 template <class F>
 PyObject *guarded(F &&f) {
     try {
@@ -203,8 +220,7 @@ PyObject *attn_decode_paged(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         void *out;
         const auto on = launch_stream(a[16], c.dev);
         if (a[14] == Py_None) {
-            made = at::empty_like(THPVariable_Unpack(a[8]));
-            if (a[16] != Py_None) made.record_stream(on);  // memory of the current stream, written on another
+            made = empty_for(on, {c.batch, hs, kDv}, at::TensorOptions().dtype(at::kBFloat16).device(at::kCUDA, c.dev));
             out = made.data_ptr();
         } else {
             out = dense(a[14], "out", at::kBFloat16, {c.batch, hs, kDv}, c.dev);
@@ -218,8 +234,7 @@ PyObject *attn_decode_paged(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
             ws = w.data_ptr();
             ws_bytes = w.nbytes();
         } else if ((ws_bytes = workspace_fn(static_cast<int>(c.batch), static_cast<int>(c.heads), most, window, sinks)) > 0) {
-            scratch = at::empty({static_cast<int64_t>(ws_bytes)}, THPVariable_Unpack(a[8]).options().dtype(at::kByte));
-            if (a[16] != Py_None) scratch.record_stream(on);
+            scratch = empty_for(on, {static_cast<int64_t>(ws_bytes)}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, c.dev));
             ws = scratch.data_ptr();
         }
         gdla_status_t st;

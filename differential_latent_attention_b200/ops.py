@@ -4,6 +4,11 @@ by a CPython extension (csrc/gdla_binding.cpp).
 Every step of the GDLA core runs in the library's CUDA kernels; PyTorch only
 provides device memory and the current CUDA stream. There is no fallback: if
 libgdla.so is missing or cannot be loaded, every call raises.
+
+Every call takes ``stream`` (a torch.cuda.Stream; the current one when not given).
+The caller orders the launch stream after the inputs and whatever reads the results
+after the launch stream; memory that a call makes itself (results and workspaces
+that were not given) is safe on both.
 """
 from __future__ import annotations
 
@@ -135,13 +140,22 @@ def _on_one_device(stream, named):
         raise ValueError(f"the tensors are on cuda:{dev} but the launch stream is on cuda:{sdev}")
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory that a call makes itself, for kernels on ``stream``. The allocator hands out a freed block as soon as its
+    own stream's order allows, so memory of the current stream may still be in use there when another stream writes
+    it: it comes from the launch stream's blocks. The caller has it on the current stream, which is made known to the
+    allocator for the day it is freed."""
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _scratch(nbytes, device, stream):
-    """Workspace of a call that was given none. The allocator may hand the memory on as soon as the call returns, so a
-    launch stream other than the current one is made known to it."""
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+    """Workspace of a call that was given none."""
+    return _empty(max(nbytes, 1), torch.uint8, device, stream)
 
 
 def _check_workspace(ws):
@@ -187,7 +201,7 @@ def attn_fwd(q_sig, q_noise, k, v, lam, gate, seqlens, window=0, out=None, strea
     _check(lam, "lam", torch.float32, (n, hs))
     _check(gate, "gate", torch.bfloat16, (n, hs, DV))
     if out is None:
-        out = torch.empty_like(gate)
+        out = _empty(gate.shape, gate.dtype, gate.device, stream)
     _check(out, "out", torch.bfloat16, (n, hs, DV))
     _on_one_device(stream, (("q_sig", q_sig), ("q_noise", q_noise), ("k", k), ("v", v), ("lam", lam),
                             ("gate", gate), ("out", out)))
@@ -236,7 +250,7 @@ def attn_bwd(q_sig, q_noise, k, v, lam, gate, dout, seqlens, window=0, grads=Non
               "dk": ((n, hkv, DQK), torch.bfloat16), "dv": ((n, hkv, DV), torch.bfloat16),
               "dlambda": ((n, hs), torch.float32), "dgate": ((n, hs, DV), torch.bfloat16)}
     if grads is None:
-        grads = {name: torch.empty_like(t) for name, t in zip(shapes, (q_sig, q_noise, k, v, lam, gate))}
+        grads = {name: _empty(shape, dt, q_sig.device, stream) for name, (shape, dt) in shapes.items()}
     for name, (shape, dt) in shapes.items():
         _check(grads[name], name, dt, shape)
     need = attn_bwd_sinks_workspace_bytes(lens, hkv, window, sinks) if sinks else attn_bwd_workspace_bytes(n, hkv)
@@ -289,7 +303,7 @@ def prologue(x, w_qa, w_kva, gamma_q, gamma_kv, w_qb, w_uk, w_uv, w_lambda, w_ga
               "k": ((n, hkv, DQK), torch.bfloat16), "v": ((n, hkv, DV), torch.bfloat16),
               "lam": ((n, hs), torch.float32), "gate": ((n, hs, DV), torch.bfloat16)}
     if outs is None:
-        outs = {name: torch.empty(shape, dtype=dt, device=x.device) for name, (shape, dt) in shapes.items()}
+        outs = {name: _empty(shape, dt, x.device, stream) for name, (shape, dt) in shapes.items()}
     for name, (shape, dt) in shapes.items():
         _check(outs[name], name, dt, shape)
     if workspace is None:
@@ -334,7 +348,7 @@ def attn_decode(q_sig, q_noise, k_cache, v_cache, cu_seqlens_k, max_seqlen_k, la
     _check(lam, "lam", torch.float32, (b, hs))
     _check(gate, "gate", torch.bfloat16, (b, hs, DV))
     if out is None:
-        out = torch.empty((b, hs, DV), dtype=torch.bfloat16, device=q_sig.device)
+        out = _empty((b, hs, DV), torch.bfloat16, q_sig.device, stream)
     _check(out, "out", torch.bfloat16, (b, hs, DV))
     need = decode_workspace_bytes(b, hkv, max_seqlen_k, window)
     if workspace is None and need > 0:
@@ -379,7 +393,7 @@ def attn_decode_latent(q_abs_sig, q_abs_noise, ckv, cu_seqlens_k, max_seqlen_k, 
     _check(lam, "lam", torch.float32, (b, hs))
     _check(gate, "gate", torch.bfloat16, (b, hs, DV))
     if out is None:
-        out = torch.empty((b, hs, DV), dtype=torch.bfloat16, device=q_abs_sig.device)
+        out = _empty((b, hs, DV), torch.bfloat16, q_abs_sig.device, stream)
     _check(out, "out", torch.bfloat16, (b, hs, DV))
     need = decode_latent_workspace_bytes(b, hkv, max_seqlen_k, window)
     if workspace is None and need > 0:
