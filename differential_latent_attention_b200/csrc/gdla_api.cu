@@ -263,13 +263,15 @@ gdla_status_t check_seqlens(int batch, const int32_t *seqlens, int num_kv_heads,
     return GDLA_OK;
 }
 
-// Sinks count behind a window alone. A window that reaches over the longest sequence
+// Sinks count behind a window alone. With sinks, a window that reaches over the longest sequence
 // is the full causal mask.
-gdla_status_t check_sinks(int longest, int *window, int *sinks) {
+gdla_status_t check_mask(int longest, int *window, int *sinks) {
     if (*sinks < 0) return GDLA_ERR_INVALID_ARG;
     if (*sinks > GDLA_MAX_SINKS) return GDLA_ERR_UNSUPPORTED;
     if (*sinks > 0 && *window >= longest) *window = 0;
     if (*window <= 0) *sinks = 0;
+    // as good as any larger window in the same schedule, and what is added to it stays in 32 bits
+    *window = std::min(*window, std::max(longest, kPrefillSlidingMaxWindow + 1));
     // item codes carry the tile in 20 bits
     if (*sinks > 0 && longest > (static_cast<int>(kItemTileMask) + 1) * kPrefillTileTokens) return GDLA_ERR_UNSUPPORTED;
     return GDLA_OK;
@@ -352,7 +354,7 @@ static gdla_status_t attn_fwd(const void *q_sig, const void *q_noise, const void
     long long n_total = 0;
     int longest = 0;
     gdla_status_t st = check_seqlens(batch, seqlens, num_kv_heads, &n_total, &longest);
-    if (st == GDLA_OK) st = check_sinks(longest, &window, &sinks);
+    if (st == GDLA_OK) st = check_mask(longest, &window, &sinks);
     if (st != GDLA_OK) return st;
     if (n_total == 0) return GDLA_OK;
     if (!aligned16(q_sig) || !aligned16(q_noise) || !aligned16(k) || !aligned16(v) || !aligned16(lambda) ||
@@ -424,7 +426,7 @@ static gdla_status_t attn_bwd(const void *q_sig, const void *q_noise, const void
     long long n_total = 0;
     int longest = 0;
     gdla_status_t status = check_seqlens(batch, seqlens, num_kv_heads, &n_total, &longest);
-    if (status == GDLA_OK) status = check_sinks(longest, &window, &sinks);
+    if (status == GDLA_OK) status = check_mask(longest, &window, &sinks);
     if (status != GDLA_OK) return status;
     if (n_total == 0) return GDLA_OK;
     if (!aligned16(q_sig) || !aligned16(q_noise) || !aligned16(k) || !aligned16(v) || !aligned16(lambda) ||
@@ -557,7 +559,7 @@ size_t gdla_attn_bwd_sinks_workspace_bytes(int batch, const int32_t *seqlens, in
         long long n_total = 0;
         int longest = 0;
         gdla_status_t st = check_seqlens(batch, seqlens, num_kv_heads, &n_total, &longest);
-        if (st == GDLA_OK) st = check_sinks(longest, &window, &sinks);
+        if (st == GDLA_OK) st = check_mask(longest, &window, &sinks);
         if (st == GDLA_OK)
             total = bwd_workspace(n_total, num_kv_heads, dkv_splits(batch, seqlens, num_kv_heads, window, sinks), sinks).total;
         return st;
