@@ -19,7 +19,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libgdla.so")
-BINDING_PATH = os.path.join(PKG, "_gdla_binding.so")
 BINDING_SOURCES = [os.path.join(CSRC, "gdla_binding.cpp"), os.path.join(INCLUDE, "gdla.h")]
 SOURCES = ["gdla_lib.cu", "gdla_api.cu", "gdla_prefill.cu", "gdla_prefill_bwd.cu", "gdla_prologue.cu", "gdla_decode.cu", "gdla_decode_noalloc.cu",
            "gdla_decode_latent.cu", "gdla_selftest.cu", "gdla_internal.h", "gdla_ptx.cuh", "gdla_prologue.h",
@@ -54,24 +53,33 @@ def _compile(cmd):
     subprocess.check_call(cmd, env={**os.environ, "TMPDIR": scratch})
 
 
+def binding_path() -> str:
+    """The binding of this interpreter and PyTorch: it reads tensors through their C++ ABI, so its name says which
+    ones it was compiled against and one made for others is not found, however new it is."""
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(PKG, f"_gdla_binding.torch-{torch.__version__}-cxx11abi{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_binding(force: bool = False) -> str:
-    """Compile csrc/gdla_binding.cpp into _gdla_binding.so next to this file."""
-    if not force and os.path.exists(BINDING_PATH):
-        t = os.path.getmtime(BINDING_PATH)
+    """Compile csrc/gdla_binding.cpp into _gdla_binding.*.so next to this file."""
+    path = binding_path()
+    if not force and os.path.exists(path):
+        t = os.path.getmtime(path)
         if all(os.path.getmtime(f) <= t for f in [*BINDING_SOURCES, __file__]):
-            return BINDING_PATH
+            return path
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
-    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     _compile(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
               "-isystem", os.path.join(base, "include"), "-isystem", os.path.join(base, "include/torch/csrc/api/include"),
               "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
               "-o", tmp, BINDING_SOURCES[0], "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
               "-ltorch", "-ltorch_python"])
-    os.replace(tmp, BINDING_PATH)
-    return BINDING_PATH
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

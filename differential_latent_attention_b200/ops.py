@@ -421,9 +421,9 @@ def _paged():
     mod = _native
     if mod is None:
         lib = library()
-        path = _build.BINDING_PATH
+        path = _build.binding_path()
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing; build it with `python -m "
+            raise RuntimeError(f"{path} is missing (it belongs to this PyTorch and interpreter alone); build it with `python -m "
                                f"differential_latent_attention_b200._build` (no fallback path exists)")
         spec = importlib.util.spec_from_file_location("_gdla_binding", path)
         mod = importlib.util.module_from_spec(spec)
