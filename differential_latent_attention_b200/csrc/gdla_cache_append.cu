@@ -33,6 +33,8 @@ namespace gdla {
 // Units: the pages that the call touches, found without the host. Sequence b owns units
 // cu[b] / P + 2 b .. cu[b + 1] / P + 2 (b + 1) - 1, which is room for the
 // floor(n / P) + 2 pages that n tokens can touch; the units that it leaves over do nothing.
+// (Where cu descends the ranges overlap and a unit goes to one of their sequences: what it finds there is checked
+// as ever, but another sequence's page may find no unit.)
 struct AppendUnit {
     bool fits;           // the unit has tokens (its page is still to be checked)
     int page;            // page of the pool

@@ -443,7 +443,7 @@ def cache_append(k_nope, k_rope, v, k_pages, v_pages, block_table, cu_seqlens_ne
     prologue's k goes in as ``k[..., :128]`` and ``k[:, 0, 128:]`` with rotate=False.
     k_pages [P, H, page_size, 192] and v_pages [P, H, page_size, 128] are bf16 or
     float8_e4m3fn, the latter with k_scale and v_scale fp32 [P, H]. The int32 CUDA
-    tensors block_table [B, W], cu_seqlens_new [B+1] and seqlens_k [B] say where: the
+    tensors block_table [B, W], cu_seqlens_new [B+1] (which must not descend) and seqlens_k [B] say where: the
     rows cu_seqlens_new[b]..cu_seqlens_new[b+1]-1 become the last positions of sequence
     b, which then holds seqlens_k[b] tokens. ``rotate`` turns k_rope to each token's
     position on the way. Pages and scales are updated in place.

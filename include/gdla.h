@@ -350,11 +350,14 @@ GDLA_API gdla_status_t gdla_attn_decode_noalloc(const void *q_sig, const void *q
  * scale (its own must be a power of two, as this call writes them). A page whose slot
  * 0 is written takes the new tokens' scale alone. NaN and infinities become e4m3's NaN.
  * Slots that get no token, and pages that no sequence's new tokens fall in, are left
- * as they were. A sequence whose entries do not fit (a negative count or length, more
+ * as they were. A sequence whose entries do not fit (a negative length, more
  * positions than its row of the table has, rows outside 0 .. num_new_tokens) and
- * table entries outside 0 .. num_pages-1 are skipped. A page that this call writes
- * must belong to one sequence: two that write one page in the same call leave that
- * page undefined. Inputs and the cache must not overlap.
+ * table entries outside 0 .. num_pages-1 are skipped. cu_seqlens_new must not descend: the
+ * sequences are found by a search over it, so with one that does, any of the call's
+ * pages may be skipped, those of sequences that fit by themselves among them (no other
+ * page is touched). A page that this call writes must belong to one sequence: two that
+ * write one page in the same call leave that page undefined. Inputs and the cache must
+ * not overlap.
  * Errors: GDLA_ERR_INVALID_ARG (null or misaligned pointers, strides, sizes < 1, an
  * unknown cache_type, num_pages * num_kv_heads or max_pages_per_seq * page_size
  * >= 2^31, batch * num_kv_heads >= 2^24), GDLA_ERR_UNSUPPORTED (num_kv_heads or page_size), GDLA_ERR_CUDA.
