@@ -273,10 +273,10 @@ __device__ __forceinline__ void append_few(const AppendPlan &p, const AppendUnit
     }
 }
 
-// One CTA per (unit, heads_per_cta heads); a unit of few rows goes to its warps, one head each. Otherwise a page and head's new values stay in registers
-// between the search for the largest and the writing, so each input is read once; the turned rotary
-// key is shared by the CTA's heads. NI = page_size / 16: 16-byte pieces of K's content (and of
-// V) per thread.
+// One CTA per (unit, heads_per_cta heads); a unit of few rows goes to its warps, one head each. Otherwise a page
+// and head's new values stay in registers between the search for the largest and the writing, so each input is
+// read once; the turned rotary key is shared by the CTA's heads. NI = page_size / 16: 16-byte pieces of K's
+// content (and of V) per thread.
 template <bool E4M3, int NI>
 __global__ void __launch_bounds__(256, NI <= 4 ? 3 : 2)
 gdla_cache_append_kernel(const __grid_constant__ AppendPlan p, float per_unit) {
@@ -429,7 +429,8 @@ cudaError_t launch_cache_append(const AppendPlan &plan, bool e4m3, cudaStream_t 
         heads = std::max(8ll, pairs / (3 * kPlanSms));
     else if (pairs >= 32ll * kPlanSms || p.num_tokens <= 16ll * p.batch)
         heads = std::max(heads, 4ll);
-    if (p.num_tokens > p.batch && p.num_tokens <= 4ll * p.batch) heads = std::max(heads, std::min(8ll, pairs / (6 * kPlanSms)));
+    if (p.num_tokens > p.batch && p.num_tokens <= 4ll * p.batch)
+        heads = std::max(heads, std::min(8ll, pairs / (6 * kPlanSms)));
     p.heads_per_cta = static_cast<int>(std::max(1ll, std::min(heads, std::min<long long>(p.hkv, pairs / kPlanSms))));
     const float per_unit = static_cast<float>(p.batch) / static_cast<float>(units);
     const unsigned grid = static_cast<unsigned>(units * ((p.hkv + p.heads_per_cta - 1) / p.heads_per_cta));

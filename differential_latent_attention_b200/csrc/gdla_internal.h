@@ -65,7 +65,8 @@ struct DkvSplit {
 
 // Passed by value (kernel parameters): the q-tiles of one launch, heaviest
 // first. The host builds the largest form and launches the smallest capacity
-// that holds the plan, so a launch carries ~3.3 KB, ~8.7 KB or ~26.6 KB.
+// that holds the plan, so a launch carries 3.6, 9.2 or 28.7 KB (0.3, 0.5 or
+// 2.1 KB of it the places of the partials, which only a backward with sinks reads).
 template <int MAX_ITEMS, int MAX_SEQS>
 struct PrefillPlanT {
     static constexpr int kMaxItems = MAX_ITEMS;

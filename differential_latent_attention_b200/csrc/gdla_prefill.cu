@@ -24,6 +24,9 @@
 //     softmax_x       one warpgroup per tile, one TMEM lane per row: online
 //                     max/sum, P = exp2(.) rounded to bf16 into TMEM over S_x
 //     O_x += P_x V    tcgen05 with A = P from TMEM, B = V from smem (MN-major)
+// P is rounded to bf16 once, as V's own type in the product: the output is 2.3e-3 to 2.5e-3 (rms, of its size) from
+// 64 bits where its own rounding alone gives 1.66e-3. Carrying the remainder as a second product would double PV,
+// which the tensor-bound full-causal path has no room for.
 // S is double-buffered per tile, so QK^T of key tile k+1 is queued while the
 // softmax of tile k runs; with two q tiles the softmax warpgroups alternate
 // (ping-pong). Epilogue: every warp finalises its rows (O/l), passes each
