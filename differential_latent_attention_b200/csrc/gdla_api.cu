@@ -188,6 +188,7 @@ bool run_plans(int batch, const int32_t *seqlens, int hkv, int window, int sinks
         }
         for (int s : used) local[s] = -1;
         P.n_seqs = n_seq;
+        P.n_rows = static_cast<int>(s0);
         if (!launch(P)) return false;
     }
     return true;
@@ -244,6 +245,12 @@ bool make_sink_maps(SinkMaps<true> *m, const void *k, const void *v, int hkv, ui
     if (first == 0) return true;
     return make_map(&m->k_sink, k, 192, hkv, n, 64, 1, first) && make_map(&m->k_rest, k, 192, hkv, n, 64, 1, rest) &&
            make_map(&m->v_sink, v, 128, hkv, n, 64, 1, first) && make_map(&m->v_rest, v, 128, hkv, n, 64, 1, rest);
+}
+
+bool make_end_maps(EndMaps *m, const void *v, int hkv, uint64_t n) {
+    for (int i = 0; i < 6; ++i)
+        if (!make_map(&m->v[i], v, 128, hkv, n, 64, 1, 1u << i)) return false;
+    return true;
 }
 
 // What every prefill call checks of its lengths; *total and *longest are filled in.
@@ -381,6 +388,7 @@ static gdla_status_t attn_fwd(const void *q_sig, const void *q_noise, const void
          !make_map(&L.tm_out, out, 128, 4 * hkv, N, 64, 4, TQ)))
         return GDLA_ERR_CUDA;
     if (sinks > 0 && !make_sink_maps(&L.sink, k, v, hkv, N, sinks, geo.key_tile)) return GDLA_ERR_CUDA;
+    if (batch > 1 && !make_end_maps(&L.end, v, hkv, N)) return GDLA_ERR_CUDA;
     L.lambda = lambda;
     L.gate = static_cast<const __nv_bfloat16 *>(gate_logits);
     L.out = static_cast<__nv_bfloat16 *>(out);
@@ -455,6 +463,7 @@ static gdla_status_t attn_bwd(const void *q_sig, const void *q_noise, const void
         !make_map(&F.tm_v, v, 128, hkv, N, 64, 1, geo.v_box))
         return GDLA_ERR_CUDA;
     if (sinks > 0 && !make_sink_maps(&F.sink, k, v, hkv, N, sinks, geo.key_tile)) return GDLA_ERR_CUDA;
+    if (batch > 1 && !make_end_maps(&F.end, v, hkv, N)) return GDLA_ERR_CUDA;
     F.lambda = lambda;
     F.gate = static_cast<const __nv_bfloat16 *>(gate_logits);
     F.bwd = {static_cast<const __nv_bfloat16 *>(dout), static_cast<__nv_bfloat16 *>(dgate), dlambda, dh_sig, dh_noise,

@@ -58,6 +58,13 @@ struct SinkMaps<true> {
     CUtensorMap k_sink, k_rest, v_sink, v_rest;
 };
 
+// Tensor maps of V in boxes of 1, 2, 4, 8, 16 and 32 rows: the tile in which a sequence ends is loaded up to its last row
+// with them, and filled with zeros (rows past the tensor) behind it. The whole tile's box would run on into the
+// next sequence, whose weights here are zero; but zero times an infinity or a NaN is NaN.
+struct EndMaps {
+    CUtensorMap v[6];
+};
+
 // How the dK, dV kernel with sinks cuts its items (see the backward below).
 struct DkvSplit {
     int chunks, chunk_steps, sink_steps;
@@ -76,6 +83,7 @@ struct PrefillPlanT {
     int window;
     int sinks;                // first tokens visible behind the window (0 with window <= 0)
     int n_seqs;
+    int n_rows;               // packed rows of the call
     int seq_start[MAX_SEQS];  // packed row of each sequence's first token
     int seq_len[MAX_SEQS];
     DkvSplit split;           // dkv with sinks
@@ -104,6 +112,7 @@ struct BwdIO {
 struct PrefillLaunch {
     CUtensorMap tm_qs, tm_qn, tm_k, tm_v;
     SinkMaps<true> sink;                  // with sinks
+    EndMaps end;
     CUtensorMap tm_gate, tm_lam, tm_out;  // used by the asynchronous epilogue (short windows)
     const float *lambda;
     const __nv_bfloat16 *gate;

@@ -39,6 +39,18 @@
 
 namespace gdla {
 
+// Rows r0 .. r1 - 1 of `chunks` chunks of 128-byte rows in shared memory become zero, by `threads` threads of which
+// this is `t`, before the arrival of each that lets the MMA warp read them. A sequence's last tile (or step) runs on into
+// the next sequence: those rows' weights are zero, but zero times an infinity or a NaN there would be NaN here. The
+// warps that make the weights do it where a sequence ends; in the MMA warp the test alone took 1 to 3 % of a call.
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int chunks, int chunk_bytes, int r0, int r1, int t, int threads) {
+    for (int c = 0; c < chunks; ++c) {
+        uint4 *rows = reinterpret_cast<uint4 *>(tile + c * chunk_bytes + r0 * 128);
+        for (int i = t; i < (r1 - r0) * 8; i += threads) rows[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+}
+
 namespace pb {
 constexpr int TOK = kPrefillTileTokens;  // 24
 constexpr int DQK = 192, DV = 128;
@@ -389,6 +401,9 @@ gdla_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_const
                     pk[i] = pack_bf16x2(ds2[0], ds2[1]);
                 }
                 tmem_st16(s_addr, pk);
+                const int own = it.L - (it.kv_lo - it.pre + k * BN);  // rows of the tile that are the sequence's
+                if (own < BN)
+                    zero_rows(smem + OFF_KV + step % STAGES * STAGE, 3, KV_CHUNK, own, BN, threadIdx.x, 32 * ROW_WARPS);
                 tc_fence_before();
                 mbar_arrive(ds_full + b);
             }
@@ -463,6 +478,14 @@ constexpr int NUM_THREADS = 32 * KEY_WARPS + 64;
 constexpr int PRODUCER_WARP = KEY_WARPS, MMA_WARP = KEY_WARPS + 1;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 }  // namespace pbk
+
+// The rows of Q and dH in a step's stage that belong to tokens `own` .. 11. Out of line: inlined, its registers cost the
+// loop of the key warps 2 to 4 % (4,096 tokens, window 1,000: 1,221 -> 1,266 us).
+__device__ __noinline__ void zero_step_tail(uint8_t *stage, int own) {
+    using namespace pbk;
+    zero_rows(stage, 5, H_CHUNK, 4 * own, STEP_SIG_ROWS, threadIdx.x, 32 * KEY_WARPS);
+    zero_rows(stage, 5, H_CHUNK, STEP_NOISE_ROW0 + own, STEP_PAD_ROW0, threadIdx.x, 32 * KEY_WARPS);
+}
 
 template <class Plan, bool SINK>
 __global__ void __launch_bounds__(pbk::NUM_THREADS, 1)
@@ -781,6 +804,7 @@ gdla_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_qs, const __grid_cons
                     dk2[14] = dk2[15] = 0u;
                 }
                 tmem_st16x2(s_addr, pk, s_addr + 16, dk2);
+                if (th + HT > it.L) zero_step_tail(smem + OFF_ST + st * STAGE, it.L - th);
                 tc_fence_before();
                 mbar_arrive(pds_full + b);
             }
@@ -954,6 +978,7 @@ static cudaError_t with_sized_plan(const PrefillPlan &plan, F &&launch) {
         small.window = plan.window;
         small.sinks = plan.sinks;
         small.n_seqs = plan.n_seqs;
+        small.n_rows = plan.n_rows;
         std::memcpy(small.seq_start, plan.seq_start, sizeof(int) * plan.n_seqs);
         std::memcpy(small.seq_len, plan.seq_len, sizeof(int) * plan.n_seqs);
         small.split = plan.split;

@@ -94,6 +94,9 @@ typedef enum {
  *   num_kv_heads 1 .. GDLA_MAX_KV_HEADS
  *   window       <= 0: full causal; > 0: query t sees keys t-window+1 .. t
  *   stream       cudaStream_t to enqueue on
+ * What one sequence holds never shows in another's rows, infinities and NaN included
+ * (nor in the gradients of the calls below). Inside a sequence a non-finite K or V can
+ * also show in rows that do not see it: their weights are zero, 0 * NaN is not.
  * Errors: GDLA_ERR_INVALID_ARG for a null or non-16-byte-aligned pointer
  * (when N > 0), batch < 1, a negative length or N >= 2^31;
  * GDLA_ERR_UNSUPPORTED for num_kv_heads out of range; GDLA_ERR_CUDA if a
@@ -222,6 +225,8 @@ GDLA_API size_t gdla_decode_workspace_bytes(int batch, int num_kv_heads, int max
  *   gate_logits  bf16 [batch, 4*num_kv_heads, 128]
  *   out          bf16 [batch, 4*num_kv_heads, 128], written
  *   window       <= 0: full context; > 0: the last `window` cache rows
+ *   (cache rows are finite: an infinity or a NaN in a sequence's first rows can also
+ *   show in the sequence packed before it; gdla_attn_decode_paged has no such limit)
  *   workspace    DEVICE scratch of at least
  *                gdla_decode_workspace_bytes(batch, num_kv_heads,
  *                max_seqlen_k, window) bytes, 256-byte aligned (may be NULL
@@ -267,6 +272,7 @@ GDLA_API gdla_status_t gdla_attn_decode(const void *q_sig, const void *q_noise, 
  *   num_kv_heads 1 .. 16 (all 5 * num_kv_heads query heads of a sequence share
  *                one CTA)
  *   window       <= 0: full context; > 0: the last `window` cache rows
+ *   (cache rows are finite, as for gdla_attn_decode)
  *   workspace    DEVICE scratch of at least gdla_decode_latent_workspace_bytes(
  *                batch, num_kv_heads, max_seqlen_k, window) bytes, 256-byte
  *                aligned; its contents need no initialisation
