@@ -334,7 +334,7 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
     // them. Held are 1 / unit (0: no page yet) and the least unit.
     constexpr float kBias = 512.f, kRatioMin = kBias / 16.f, kRatioMax = kBias * 4.f;
     constexpr float kUnitDrop = 2.6469779601696886e-23f;  // 2^-75
-    float vs_inv = 0.f, vs_floor = 0.f;
+    float vs_inv = 0.f, vs_floor = 1e-35f;  // (kBias over a smaller unit would leave fp32)
     for (int n = 0; n < mine; ++n) {
         const int st = n % STAGES;
         const uint8_t *kb = ring + st * C::STAGE, *vb = kb + C::K_BYTES;
@@ -418,7 +418,7 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
             if constexpr (E4M3) {
                 float ratio = a.w * vs_inv;
                 const float size = fabsf(a.w);
-                if (!(fabsf(ratio) >= kRatioMin && fabsf(ratio) <= kRatioMax) && size >= 1e-35f) {
+                if (!(fabsf(ratio) >= kRatioMin && fabsf(ratio) <= kRatioMax) && size > 0.f) {
                     const float unit = fmaxf(size, vs_floor), inv = kBias / unit, f = vs_inv > 0.f ? inv / vs_inv : 1.f;
 #pragma unroll
                     for (int mt = 0; mt < DV / 16; ++mt)

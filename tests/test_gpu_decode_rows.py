@@ -65,6 +65,15 @@ def test_values_times_a_power_of_two(lens, heads):
         assert torch.equal(got.float(), ref.float() * 2.0 ** e), e
 
 
+@pytest.mark.parametrize("e", [-118, -100, 110])
+def test_values_near_the_ends_of_fp32(e):
+    """V scales down to 2^-127 (an fp32 subnormal, smaller than any that the append writes) and up to 2^104."""
+    lens = [1, 17, 300, 2049]
+    d, pool, table = _case(lens, 2, 32, "e4m3", 931)
+    pool["v_scale"] *= 2.0 ** e
+    check_rows(_run(d, pool, table, lens), plain_decode(**d, pool=pool, table=table, page=32, lens=lens), e)
+
+
 def _dominated(above, apart, size, neighbours):
     """160 sequences of 2,000 keys (one CTA an item: every warp's sums matter) whose first key scores `above` log2 units
     over the others by dim 0 alone, and whose first page has no values and a V scale 2^apart times the other pages'."""
