@@ -10,11 +10,12 @@
 // sigmoid gate (aitrends.kr/articles/94908, GDLA paragraphs).
 //
 // HBM bounds it where there are keys enough: 320 B (e4m3) or 640 B (bf16) per key and KV head against 3,200
-// flops, 10 per byte. Measured on one B200: 64 sequences of 1,024 to 32,768 e4m3 tokens, 16 heads: 855 us, 6.8 TB/s
-// (a copy runs at 6.5, reads alone somewhat faster). Short or few sequences are bound by the chain of a warp's
+// flops, 10 per byte. Measured on one B200: 64 sequences of 1,024 to 32,768 e4m3 tokens, 16 heads: 862 us, 6.8 TB/s,
+// alone (a copy runs at 6.5, reads alone somewhat faster), 913 to 1,000 call after call, at the card's power cap. Short or few sequences are bound by the chain of a warp's
 // start (length, page, first rows: 2 us), blocks (1.0 to 1.4 us each, their loads under way meanwhile) and join
-// (1 us in the CTA, 1.5 over a cluster): one sequence of 4,096 bf16 tokens 13.9 us, 64 with window 128 and 4 sinks
-// 22.4 us (floors 6.5 and 14.0).
+// (1 us in the CTA, 1.5 over a cluster): one sequence of 4,096 bf16 tokens 14 us in a graph, 16.3 as
+// called, 64 with window 128 and 4 sinks 22.4 and 24.4 us (floors 6.5 and 14.0; a fifth of the latter's traffic is
+// rows of the copied blocks that nobody sees).
 //
 // Keys come in blocks of 16 that never straddle a page (pages are multiples of 16), so
 // a block has one scale for K and one for V. The products are mma.sync m16n8k16 with the
