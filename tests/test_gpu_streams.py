@@ -75,25 +75,30 @@ def _segment_stream(t):
 def test_blocks_with_work_pending_are_left_alone(name):
     """Blocks of the sizes that the call needs were freed on the current stream while it still has to write them."""
     call, side = CALLS[name](), torch.cuda.Stream()
-    got = call(None)
-    ref = _copies(got)
+    ref = _copies(call(None))
     for x in call(side).values():    # the side stream's own blocks are there, and the kernels that the test runs itself
         x.view(torch.uint8).fill_(0xFF)
     torch.cuda._sleep(1000)
     torch.cuda.synchronize()
-    torch.cuda._sleep(BUSY)
-    for x in got.values():
-        x.view(torch.uint8).fill_(0xFF)
-    del got, x
-    busy = torch.cuda.Event()
-    busy.record()
-    got = call(side)
-    side.synchronize()
-    assert not busy.query()          # the current stream had not come to its writes yet
-    torch.cuda.synchronize()
-    assert all(_segment_stream(x) == side.cuda_stream for x in got.values())
-    assert gdla.device_error() == 0
-    assert _same(got, ref)
+    for attempt in range(3):
+        got = call(None)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(BUSY << attempt)
+        for x in got.values():
+            x.view(torch.uint8).fill_(0xFF)
+        del got, x
+        busy = torch.cuda.Event()
+        busy.record()
+        got = call(side)
+        side.synchronize()
+        before = not busy.query()    # the current stream had not come to its writes yet
+        torch.cuda.synchronize()
+        assert all(_segment_stream(x) == side.cuda_stream for x in got.values())
+        assert gdla.device_error() == 0
+        assert _same(got, ref)
+        if before:
+            return
+    pytest.skip("the host was too slow for the order of writes that this test wants")
 
 
 @pytest.mark.parametrize("name", CALLS)
