@@ -13,10 +13,11 @@
 // scale moves only where its smallest numbers begin) and keeps those divisions exact.
 //
 // Bytes alone bound it: 8,320 read and 5,120 (e4m3, 16 heads) or 10,240 (bf16) written per token.
-// Measured on one B200 (16 heads): 32,600 tokens into e4m3 pages of 64 82 us in a graph, 84 to 88 as called (5.3 and 5.1 TB/s of 6.5 TB/s copied), held
-// by the conversions beside the loads (59 % of the issue slots); a step of 64 sequences 4.4 us (6.2 as called), of one 3.1 us (4.1), which
-// is a launch and a chain of five dependent loads (sequence, lengths, page, scale, row). One launch takes steps and
-// prompts together, each page by the rows that it gets: 63 steps beside a chunk of 65 tokens 8.6 us.
+// Measured on one B200 (16 heads), in a graph and, in brackets, as called: 32,600 tokens into e4m3 pages of 64 82 us
+// (84 to 88), 5.3 TB/s of 6.5 TB/s copied, held by the conversions beside the loads (59 % of the issue slots); a step
+// of 64 sequences 4.5 us (6.2), of one 3.1 us (4.1), which is a launch and a chain of five dependent loads (sequence,
+// lengths, page, scale, row). One launch takes steps and prompts together, each page by the rows that it gets: 63
+// steps beside a chunk of 65 tokens 8.6 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

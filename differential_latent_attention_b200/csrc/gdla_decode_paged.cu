@@ -10,12 +10,12 @@
 // sigmoid gate (aitrends.kr/articles/94908, GDLA paragraphs).
 //
 // HBM bounds it where there are keys enough: 320 B (e4m3) or 640 B (bf16) per key and KV head against 3,200
-// flops, 10 per byte. Measured on one B200: 64 sequences of 1,024 to 32,768 e4m3 tokens, 16 heads: 862 us, 6.8 TB/s,
-// alone (a copy runs at 6.5, reads alone somewhat faster), 913 to 1,000 call after call, at the card's power cap. Short or few sequences are bound by the chain of a warp's
-// start (length, page, first rows: 2 us), blocks (1.0 to 1.4 us each, their loads under way meanwhile) and join
-// (1 us in the CTA, 1.5 over a cluster): one sequence of 4,096 bf16 tokens 14 us in a graph, 16.3 as
-// called, 64 with window 128 and 4 sinks 22.4 and 24.4 us (floors 6.5 and 14.0; a fifth of the latter's traffic is
-// rows of the copied blocks that nobody sees).
+// flops, 10 per byte. Measured on one B200, alone or in a graph and, in brackets, as called: 64 sequences of 1,024 to
+// 32,768 e4m3 tokens, 16 heads: 862 us, 6.8 TB/s (913 to 1,000 at the card's power cap; a copy runs at 6.5 TB/s, reads
+// alone somewhat faster). Short or few sequences are bound by the chain of a warp's start (length, page, first rows:
+// 2 us), blocks (1.0 to 1.4 us each, their loads under way meanwhile) and join (1 us in the CTA, 1.5 over a cluster):
+// one sequence of 4,096 bf16 tokens 14.5 us (16.3), 64 with window 128 and 4 sinks 22.4 us (24.4); floors 6.5 and 14.0,
+// and a fifth of the latter's traffic is rows of the copied blocks that nobody sees.
 //
 // Keys come in blocks of 16 that never straddle a page (pages are multiples of 16), so
 // a block has one scale for K and one for V. The products are mma.sync m16n8k16 with the
@@ -329,8 +329,8 @@ gdla_decode_paged_kernel(const __grid_constant__ PagedDecode p) {
     // take kBias and the ratio of their own page's scale to that one, so that the products add straight onto O. Ratios
     // from 2^-4 to 2^2 leave an f16 probability its 11 bits down to 2^-19 of the running maximum, or further, and a step
     // of 2^-29 under that (p <= 2^kTrail, so 2^15 at most); a page further off changes the unit. Without the bias, and with
-    // ratios from 2^-8 on, a key that took nearly all the weight left the others 2^-17 of it as step: 1e-3 to
-    // 2e-2 of the output where its own value was small. The unit goes down to 2^-75 of the largest one so far at most: O,
+    // ratios from 2^-8 on, a key that took nearly all the weight left the others 2^-17 of it as step: up to a fifth
+    // of the output where its own value was small. The unit goes down to 2^-75 of the largest one so far at most: O,
     // under 2^51 of those, stays finite, and a page whose scale is smaller yet (one of zeros has 2^-110) is lost beside
     // them. Held are 1 / unit (0: no page yet) and the least unit.
     constexpr float kBias = 512.f, kRatioMin = kBias / 16.f, kRatioMax = kBias * 4.f;
